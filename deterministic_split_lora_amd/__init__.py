@@ -1,4 +1,5 @@
-"""Deterministic Split-K LoRA shrink / expand for AMD MI355X (gfx950).
+"""Deterministic Split-K LoRA shrink / expand for AMD MI355X (gfx950), and the
+operators around the adapters: MX4 products, the block norm, sampling.
 
 The computation lives in liblora_det.so (hand-written HIP kernels behind the C
 interface of include/lora_det.h); this package is its thin Python binding, with
@@ -14,4 +15,6 @@ from ._binding import (  # noqa: F401
     lora_sgmv_counter_bytes, lora_sgmv_shrink_counted, lora_shrink_expand_counter_bytes, lora_shrink_expand_counted,
     lora_expand_compensated, lora_sgmv_shrink_expand, lora_shrink_expand_noalloc, NOALLOC_SCRATCH_BYTES,
     lora_sgmv_shrink_atomic, lora_counted_workspace_bytes,
+    lora_mx4_quantize, lora_mx4_dequantize, lora_mx4_linear, lora_mx4_linear_q, lora_mx4_linear_workspace_bytes,
+    lora_block_norm, lora_sample,
 )

@@ -12,8 +12,9 @@ import sys
 HERE = os.path.dirname(os.path.abspath(__file__))
 CSRC = os.path.join(HERE, "csrc")
 LIB = os.path.join(HERE, "liblora_det.so")
-SOURCES = ["abi.hip", "shrink.hip", "expand.hip", "fused.hip", "streamed.hip", "sgmv_plan.hip"]
-HEADERS = ["device.h", "kernels.h", "shrink_tile.h"]
+SOURCES = ["abi.hip", "shrink.hip", "expand.hip", "fused.hip", "streamed.hip", "sgmv_plan.hip",
+           "abi_step.hip", "mx4.hip", "mx4_linear.hip", "block_norm.hip", "sample.hip"]
+HEADERS = ["device.h", "kernels.h", "shrink_tile.h", "step_kernels.h", "mx4.h"]
 
 HIPCC_FLAGS = [
     "--offload-arch=gfx950",

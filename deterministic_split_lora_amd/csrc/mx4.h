@@ -1,0 +1,47 @@
+// MX4 building blocks: E2M1 codes in pairs (element 2i in the low four bits of
+// byte i), one E8M0 scale byte b for kMxBlock elements, value = code 2^(b-127);
+// b = 255 makes the block NaN.
+#pragma once
+
+#include "device.h"
+#include "step_kernels.h"
+
+namespace lora {
+
+typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
+typedef int32_t i32x8 __attribute__((ext_vector_type(8)));
+typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
+
+// The scale 2^(b-127) as the fp32 operand of the conversion instructions
+// (2^-127, b = 0, is below the smallest normal fp32; b = 255 gives a NaN).
+__device__ __forceinline__ float mx_scale_f32(uint32_t b)
+{
+    const uint32_t bits = b == 0 ? 0x00400000u : (b == 255 ? 0x7FC00000u : b << 23);
+    return __builtin_bit_cast(float, bits);
+}
+
+// Eight codes (one 32-bit word) as bf16, times the scale.  Exact: a code has two
+// significant bits.
+__device__ __forceinline__ bf16x8 mx4_to_bf16(uint32_t w, float scale)
+{
+    const bf16x2 a = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w, scale, 0);
+    const bf16x2 b = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w, scale, 1);
+    const bf16x2 c = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w, scale, 2);
+    const bf16x2 d = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w, scale, 3);
+    return bf16x8{a[0], a[1], b[0], b[1], c[0], c[1], d[0], d[1]};
+}
+
+// Eight bf16 (in pairs) divided by the scale, as codes: nearest, ties to even,
+// saturated at 6.  (The words are copied out first: a bit cast straight from a
+// vector's element reads its first element.)
+__device__ __forceinline__ uint32_t bf16_to_mx4(u32x4 v, float scale)
+{
+    const uint32_t v0 = v[0], v1 = v[1], v2 = v[2], v3 = v[3];
+    uint32_t w = 0;
+    w = __builtin_amdgcn_cvt_scalef32_pk_fp4_bf16(w, __builtin_bit_cast(bf16x2, v0), scale, 0);
+    w = __builtin_amdgcn_cvt_scalef32_pk_fp4_bf16(w, __builtin_bit_cast(bf16x2, v1), scale, 1);
+    w = __builtin_amdgcn_cvt_scalef32_pk_fp4_bf16(w, __builtin_bit_cast(bf16x2, v2), scale, 2);
+    return __builtin_amdgcn_cvt_scalef32_pk_fp4_bf16(w, __builtin_bit_cast(bf16x2, v3), scale, 3);
+}
+
+}  // namespace lora

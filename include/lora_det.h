@@ -495,6 +495,128 @@ int lora_sgmv_expand(const float* h, int64_t ld_h, const uint16_t* const* B_ptrs
                      int32_t n_adapters, uint16_t* y, int64_t ld_y,
                      int64_t M, int64_t N, int32_t r_max, void* stream);
 
+/* ---------------------------------------------------------------------------
+ * The operators around the adapters: what a decode or prefill step of an
+ * adapted model computes besides the shrink and the expand.  Same conventions
+ * (ownership, errors, streams), and the same promise: each output row's bits
+ * depend only on that row's own inputs and the sizes named below, not on M or
+ * B, on the other rows, on the stream or on timing.
+ *
+ * MX4: microscaled 4-bit floating point.  A row of K values (K % 32 == 0) is
+ * cut into blocks of 32; a block has one scale byte b and 32 codes of 4 bits.
+ *   code  sign (bit 3) and magnitude 0, 0.5, 1, 1.5, 2, 3, 4, 6 (bits 2..0)
+ *   value = code * 2^(b - 127);  b = 255: the block is NaN
+ *   q       uint8 [rows][ld_q bytes]: element 2i in the low and 2i + 1 in the
+ *           high four bits of byte i; 16-byte aligned, ld_q % 16 == 0,
+ *           ld_q >= K / 2
+ *   scales  uint8 [rows][ld_s bytes]: byte j for elements 32j .. 32j + 31;
+ *           4-byte aligned, ld_s % 4 == 0, ld_s >= K / 32 (so every row's last
+ *           aligned word can be read; bytes past K / 32 are ignored and left
+ *           as they are)
+ * ------------------------------------------------------------------------- */
+
+/*
+ * Quantise the rows of a bf16 matrix (weights once, activations per step):
+ *   e = max(floor(log2 max|v|) - 2, -127),  b = e + 127,
+ *   code = nearest of the eight magnitudes to |v| 2^-e, ties to the code whose
+ *   last bit is 0, magnitudes above 6 become 6; the sign is kept (also of 0).
+ * A block of zeros gets b = 0.  A block with a NaN or an infinity gets b = 255
+ * and codes 0, so that it dequantises to NaN.  One launch.
+ * x: 16-byte aligned, ld_x % 8 == 0.
+ */
+int lora_mx4_quantize(const uint16_t* x, int64_t ld_x, uint8_t* q, int64_t ld_q, uint8_t* scales, int64_t ld_s,
+                      int64_t M, int64_t K, void* stream);
+
+/* x = value of each code, rounded to bf16 (exact but beyond bf16's range).
+   One launch. */
+int lora_mx4_dequantize(const uint8_t* q, int64_t ld_q, const uint8_t* scales, int64_t ld_s,
+                        uint16_t* x, int64_t ld_x, int64_t M, int64_t K, void* stream);
+
+/*
+ * The base layer's product with MX4 weights:  y = x W^T  (the first term of
+ * Eq. 1; lora_expand and lora_sgmv_expand then add the adapter's term to y).
+ *     y[i][n] = bf16_rne( (..(C_0 + C_1) + ..) + C_{S-1} )
+ *     C_s = sum over chunk s (K / split_k consecutive k) of x[i][k] W[n][k]
+ * C_s is one chain of matrix-core steps in ascending k with an fp32
+ * accumulator; the chunks are added in ascending order in fp32.  W enters with
+ * its exact values.  A row's bits depend on x's row, W, K and split_k only,
+ * whatever kernel M and N select.  split_k = 4..16 suits few rows (the chunks
+ * run in parallel), 1 suits many (no sums to join).
+ *   lora_mx4_linear    x bf16 [M][ld_x], 16-byte aligned, ld_x % 8 == 0
+ *   lora_mx4_linear_q  x as MX4 codes and scales [M] rows
+ *   wq, ws             W as MX4 codes and scales, N rows
+ *   y                  bf16 [M][ld_y], written; 16-byte aligned, ld_y % 8 == 0
+ * split_k in {1, 2, 4, 8, 16}, K % (32 split_k) == 0, N % 8 == 0.
+ * workspace: >= lora_mx4_linear_workspace_bytes(M, K, N, split_k) bytes,
+ * 16-byte aligned, no initialisation needed (may be NULL when that is 0; 0 is
+ * also returned for invalid input).
+ */
+size_t lora_mx4_linear_workspace_bytes(int64_t M, int64_t K, int64_t N, int32_t split_k);
+
+int lora_mx4_linear(const uint16_t* x, int64_t ld_x, const uint8_t* wq, int64_t ld_wq, const uint8_t* ws,
+                    int64_t ld_ws, uint16_t* y, int64_t ld_y, int64_t M, int64_t K, int64_t N, int32_t split_k,
+                    void* workspace, size_t workspace_bytes, void* stream);
+
+int lora_mx4_linear_q(const uint8_t* xq, int64_t ld_xq, const uint8_t* xs, int64_t ld_xs, const uint8_t* wq,
+                      int64_t ld_wq, const uint8_t* ws, int64_t ld_ws, uint16_t* y, int64_t ld_y, int64_t M,
+                      int64_t K, int64_t N, int32_t split_k, void* workspace, size_t workspace_bytes,
+                      void* stream);
+
+/*
+ * The step between two blocks of a network: the norm after the block that made
+ * y, its gate, the scaled residual, the norm before the next block.
+ *     t  = post_norm(y[i])                       (y itself for LORA_NORM_NONE)
+ *     r' = res_scale * r[i] + gate[i / gate_group] * t
+ *     r_out[i] = bf16(r'),   x_out[i] = bf16(pre_norm(r'))
+ * in fp32, the pre-norm taken from r' before its rounding.
+ *     LORA_NORM_RMS    norm(v) = v / sqrt(mean(v^2) + eps) * w + b
+ *     LORA_NORM_LAYER  the same of v - mean(v)
+ * post_w, pre_w (NULL: 1) and post_b, pre_b (NULL: 0): bf16 [C].  gate: bf16
+ * [ceil(M / gate_group)][ld_gate] or NULL (1): gate_group 1 is a gate per
+ * token, T a gate per sequence of T tokens, M one for all.  y NULL: no block
+ * output, r' = res_scale * r.  x_out NULL (exactly when pre is LORA_NORM_NONE):
+ * no pre-norm.  r_out may be r, and x_out may be y, with the same leading
+ * dimension.  One launch.
+ * 8 <= C <= 32768, C % 8 == 0; pointers 16-byte aligned, leading dimensions
+ * multiples of 8.
+ */
+enum lora_norm_kind { LORA_NORM_NONE = 0, LORA_NORM_RMS = 1, LORA_NORM_LAYER = 2 };
+
+int lora_block_norm(const uint16_t* y, int64_t ld_y, int32_t post, const uint16_t* post_w, const uint16_t* post_b,
+                    const uint16_t* gate, int64_t ld_gate, int64_t gate_group, const uint16_t* r, int64_t ld_r,
+                    float res_scale, uint16_t* r_out, int64_t ld_ro, int32_t pre, const uint16_t* pre_w,
+                    const uint16_t* pre_b, uint16_t* x_out, int64_t ld_xo, int64_t M, int64_t C, float eps,
+                    void* stream);
+
+/*
+ * Draws one token per row of logits from given random numbers.  With l the
+ * row's logits (NaN counts as -inf), m their maximum and T the temperature:
+ *     w_i = rint(2^31 exp((l_i - m) * (1 / T)))     a whole number; 0 for -inf
+ * so every sum below is exact and no order of work can change the token.
+ * Tokens are ordered by (l descending, index ascending).
+ *   top_k  k <= 0 or k >= V: off; otherwise the first k are kept
+ *   top_p  p >= 1 or NaN: off; otherwise, of these, those whose predecessors
+ *          weigh less than max(ceil(p * their total weight), 1) (p <= 0: the
+ *          first)
+ *   min_p  <= 0 or NaN: off; of these, those with w_i >= min(min_p, 1) 2^31
+ * Let W be the kept weight and t = floor(u W) (at most W - 1; u <= 0 or NaN:
+ * 0), products in fp64.  The token is the lowest index whose kept weight summed
+ * over the indices up to it exceeds t.  T <= 0 or NaN: the first token of the
+ * order.  logprobs[i] = log(w_token / W), the natural logarithm of the
+ * probability it was drawn with.
+ * A row of -inf only: token -1, logprob -inf.  An infinite maximum: the logits
+ * equal to it share the weight.
+ * logits: [B][ld] bf16 (LORA_LOGITS_BF16) or fp32 (LORA_LOGITS_F32), aligned to
+ * their size, any ld >= V.  temperature, top_p, min_p, u: fp32 [B]; top_k: int32
+ * [B]; temperature NULL: 1, top_k, top_p, min_p NULL: off.  u is required, in
+ * [0, 1).  tokens: int32 [B].  logprobs: fp32 [B] or NULL.  1 <= V <= 2^22.
+ */
+enum lora_logits_type { LORA_LOGITS_BF16 = 0, LORA_LOGITS_F32 = 1 };
+
+int lora_sample(const void* logits, int32_t logits_type, int64_t ld, int64_t B, int64_t V, const float* temperature,
+                const int32_t* top_k, const float* top_p, const float* min_p, const float* u, int32_t* tokens,
+                float* logprobs, void* stream);
+
 #ifdef __cplusplus
 }
 #endif
