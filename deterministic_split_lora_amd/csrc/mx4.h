@@ -31,6 +31,21 @@ __device__ __forceinline__ bf16x8 mx4_to_bf16(uint32_t w, float scale)
     return bf16x8{a[0], a[1], b[0], b[1], c[0], c[1], d[0], d[1]};
 }
 
+constexpr int kFp4 = 4;                      // the matrix-core format selector of E2M1
+
+// One operand row's blocks of a step: codes and scale.
+struct MxOperand {
+    u32x4 q;
+    uint32_t s;
+};
+
+__device__ __forceinline__ f32x4 mfma_mx4(const MxOperand& w, const MxOperand& x, f32x4 acc)
+{
+    const i32x8 a = {(int)w.q[0], (int)w.q[1], (int)w.q[2], (int)w.q[3], 0, 0, 0, 0};
+    const i32x8 b = {(int)x.q[0], (int)x.q[1], (int)x.q[2], (int)x.q[3], 0, 0, 0, 0};
+    return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(a, b, acc, kFp4, kFp4, 0, (int)w.s, 0, (int)x.s);
+}
+
 // Eight bf16 (in pairs) divided by the scale, as codes: nearest, ties to even,
 // saturated at 6.  (The words are copied out first: a bit cast straight from a
 // vector's element reads its first element.)

@@ -13,27 +13,13 @@
 //     operands' codes and scales as they are stored.
 // The "row" operand is W, so a lane's accumulator holds four consecutive output
 // columns of one token.
-#include "mx4.h"
+#include "mx4_tile.h"
 
 namespace lora {
 
 namespace {
 
 constexpr int kStepK = 128;
-constexpr int kFp4 = 4;                      // the matrix-core format selector of E2M1
-
-// One operand row's blocks of a step: codes and scale.
-struct MxOperand {
-    u32x4 q;
-    uint32_t s;
-};
-
-__device__ __forceinline__ f32x4 mfma_mx4(const MxOperand& w, const MxOperand& x, f32x4 acc)
-{
-    const i32x8 a = {(int)w.q[0], (int)w.q[1], (int)w.q[2], (int)w.q[3], 0, 0, 0, 0};
-    const i32x8 b = {(int)x.q[0], (int)x.q[1], (int)x.q[2], (int)x.q[3], 0, 0, 0, 0};
-    return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(a, b, acc, kFp4, kFp4, 0, (int)w.s, 0, (int)x.s);
-}
 
 __device__ __forceinline__ MxOperand load_mx(const uint8_t* q, const uint8_t* s, int64_t k, bool ok)
 {
@@ -160,6 +146,11 @@ int64_t mx4_linear_workspace(int64_t M, int64_t N, int32_t k_chunk, int32_t spli
 
 hipError_t launch_mx4_linear(const Mx4LinearParams& p, bool x_is_mx4, hipStream_t st)
 {
+    if (p.M > 64 && p.k_chunk * (int64_t)p.split_k >= 512) {
+        if (p.split_k > 1)
+            return x_is_mx4 ? launch_tile<true, 128, 256, true>(p, st) : launch_tile<false, 128, 256, true>(p, st);
+        return x_is_mx4 ? launch_tile<true, 256, 256, false>(p, st) : launch_tile<false, 128, 256, false>(p, st);
+    }
     if (p.M <= 16)
         return x_is_mx4 ? launch_rows<true, 1, 1>(p, st) : launch_rows<false, 1, 1>(p, st);
     if (p.M <= 32)
