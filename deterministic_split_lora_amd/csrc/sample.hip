@@ -7,10 +7,7 @@
 //
 // Tokens are ordered by (logit descending, index ascending).  Each of top-k,
 // top-p and min-p keeps a prefix of that order, so their intersection is a
-// prefix too and is given by its last element: a threshold key and how many of
-// the elements with that very key are kept (the lowest indices).  Thresholds
-// are found by a radix select over the logits' bits, 11, 11 and 10 at a time,
-// with a histogram of counts and weights in LDS.
+// prefix too and is given by its last element.
 //
 // One workgroup owns a row.
 #include "device.h"
@@ -87,13 +84,13 @@ struct Shared {
     unsigned long long hist_w[kBins];
     unsigned long long seg[kSegs];
     uint64_t scan[2 * kWaves];
-    float red[kWaves];
     uint64_t pick_sum;
     uint64_t pick_n;
     int pick;
 };
 
-// Finds the element of the order at which a running sum (of counts when BY_N,
+// A radix select over the logits' bits, 11, 11 and 10 at a time, with a
+// histogram of counts and weights in LDS.  Finds the element of the order at which a running sum (of counts when BY_N,
 // of weights otherwise) over the elements before it is still below `target`
 // (> 0), and the next element's is not: its key, the number of elements and the
 // weight before its key.  Only elements with a weight take part.
@@ -213,43 +210,42 @@ __device__ int locate(const Row& r, Shared& s, uint64_t t, F value)
     return i;
 }
 
-__global__ void __launch_bounds__(kThreads) k_sample(SampleParams p, bool bf16)
+// One row's settings, as the definition reads them.
+struct Settings {
+    int k;                                   // 0: off
+    float top_p;                             // 1: off
+    uint32_t floor_w;                        // 0: off
+    float u;
+};
+
+// The weight a token's predecessors have to stay below.
+__device__ __forceinline__ uint64_t top_p_mass(float top_p, uint64_t total)
 {
-    __shared__ Shared s;
-    const int64_t row = blockIdx.x;
-    Row r;
-    r.bf16 = bf16;
-    r.V = p.V;
-    r.logits = static_cast<const char*>(p.logits) + row * p.ld * (bf16 ? 2 : 4);
-    const float T = p.temperature ? p.temperature[row] : 1.0f;
-    const bool greedy = !(T > 0.0f);
-    r.inv_t = greedy ? 1.0f : 1.0f / T;
+    return top_p > 0.0f ? max((uint64_t)ceil((double)top_p * (double)total), (uint64_t)1) : 1;
+}
 
-    float m = -INFINITY;
-    for (int i = threadIdx.x; i < r.V; i += kThreads)
-        m = fmaxf(m, logit(r, i));
-#pragma unroll
-    for (int d = 1; d < 64; d <<= 1)
-        m = fmaxf(m, __shfl_xor(m, d));
-    if ((threadIdx.x & 63) == 0)
-        s.red[threadIdx.x >> 6] = m;
-    __syncthreads();
-    for (int i = 0; i < kWaves; ++i)
-        m = fmaxf(m, s.red[i]);
-    r.lmax = m;
-    if (m == -INFINITY) {                    // every logit masked
-        if (threadIdx.x == 0) {
-            p.tokens[row] = -1;
-            if (p.logprobs)
-                p.logprobs[row] = -INFINITY;
-        }
-        return;
-    }
+__device__ __forceinline__ uint64_t target(float u, uint64_t total)
+{
+    const double want = u > 0.0f ? (double)u * (double)total : 0.0;
+    return want >= (double)total ? total - 1 : (uint64_t)want;
+}
 
+__device__ __forceinline__ void answer(const SampleParams& p, int64_t row, int token, uint32_t w, uint64_t total)
+{
+    p.tokens[row] = token;
+    if (p.logprobs)
+        p.logprobs[row] = logf((float)((double)w / (double)total));
+}
+
+// Any row, by passes over it: the way for what the paths below do not take
+// (more ties than their lists hold, top-k above kThreads, infinite maxima or
+// inverse temperatures).
+__device__ void sample_any(const SampleParams& p, const Settings& c, const Row& r, Shared& s, int64_t row)
+{
     // the kept prefix: keys above `key`, and of those equal to it the first `quota`
     uint32_t key = 0, quota = 0xFFFFFFFFu, ties = 0;
-    const int k = greedy ? 1 : (p.top_k ? p.top_k[row] : 0);
-    const float top_p = greedy || !p.top_p ? 1.0f : p.top_p[row];
+    const int k = c.k;
+    const float top_p = c.top_p;
     uint64_t total = 0;
     bool cut = false;
     if (k > 0 && k < r.V) {
@@ -273,7 +269,7 @@ __global__ void __launch_bounds__(kThreads) k_sample(SampleParams p, bool bf16)
     }
     // top-p needs the weight kept so far
     auto in_prefix = [&](float l) { return !cut || order_key(l) > key; };
-    if (!(top_p >= 1.0f) && top_p == top_p) {
+    if (top_p < 1.0f) {
         uint64_t mine = 0;
         uint32_t wk = 0;
         for (int i = threadIdx.x; i < r.V; i += kThreads) {
@@ -292,32 +288,27 @@ __global__ void __launch_bounds__(kThreads) k_sample(SampleParams p, bool bf16)
         __syncthreads();
         total = s.pick_sum + (cut ? (uint64_t)quota * s.pick_n : 0);
         __syncthreads();
-        const uint64_t mass = max((uint64_t)ceil((double)top_p * (double)total), (uint64_t)1);
-        if (!(top_p > 0.0f) || mass <= total) {
-            uint32_t kp, nb, tp;
-            uint64_t wb;
-            select<false>(r, s, top_p > 0.0f ? mass : 1, &kp, &nb, &wb, &tp);
-            const uint32_t u = kp ^ ((kp >> 31) ? 0x80000000u : 0xFFFFFFFFu);
-            const uint64_t wt = weight(r, __builtin_bit_cast(float, u));
-            const uint64_t need = top_p > 0.0f ? mass : 1;
-            const uint32_t qp = (uint32_t)((need - wb + wt - 1) / wt);
-            if (!cut || kp > key) {
-                key = kp;
-                quota = qp;
-                ties = tp;
-            } else if (kp == key) {
-                quota = min(quota, qp);
-            }
-            cut = true;
+        const uint64_t mass = top_p_mass(top_p, total);
+        uint32_t kp, nb, tp;
+        uint64_t wb;
+        select<false>(r, s, mass, &kp, &nb, &wb, &tp);
+        const uint32_t u = kp ^ ((kp >> 31) ? 0x80000000u : 0xFFFFFFFFu);
+        const uint64_t wt = weight(r, __builtin_bit_cast(float, u));
+        const uint32_t qp = (uint32_t)((mass - wb + wt - 1) / wt);
+        if (!cut || kp > key) {
+            key = kp;
+            quota = qp;
+            ties = tp;
+        } else if (kp == key) {
+            quota = min(quota, qp);
         }
+        cut = true;
     }
     // of the tied elements the first `quota`: up to and including column `last`
     int last = r.V;
     if (cut && quota < ties)
         last = locate(r, s, quota - 1, [&](int i) { return (uint64_t)(order_key(logit(r, i)) == key); });
-    const float min_p = greedy || !p.min_p ? 0.0f : p.min_p[row];
-    const uint32_t floor_w =
-        min_p > 0.0f ? (uint32_t)fmin(ceil((double)min_p * (double)kOne), (double)kOne) : 0u;
+    const uint32_t floor_w = c.floor_w;
     auto kept = [&](int i) -> uint64_t {
         const float l = logit(r, i);
         const uint32_t w = weight(r, l), o = order_key(l);
@@ -333,14 +324,550 @@ __global__ void __launch_bounds__(kThreads) k_sample(SampleParams p, bool bf16)
     __syncthreads();
     total = s.pick_sum;
     __syncthreads();
-    const float u = p.u[row];
-    const double want = u > 0.0f ? (double)u * (double)total : 0.0;
-    const uint64_t t = want >= (double)total ? total - 1 : (uint64_t)want;
-    const int token = locate(r, s, t, kept);
+    const int token = locate(r, s, target(c.u, total), kept);
+    if (threadIdx.x == 0)
+        answer(p, row, token, (uint32_t)kept(token), total);
+}
+
+// ---------------------------------------------------------------------------
+// The usual rows.  The row is read in aligned 16-byte groups of kVec logits;
+// wave w has the w-th contiguous run of groups, so that sums over a wave's
+// elements are sums over a range of indices.
+// ---------------------------------------------------------------------------
+constexpr int kHist = 512;                   // bins over the weights' range, per wave
+constexpr int kList = 4096;                  // elements of the bins at the threshold
+constexpr int kFew = 1024;                   // elements compared with one another
+constexpr float kRange = 22.0f;              // rint(2^31 exp(-z)) is 0 from z = 32 ln 2 = 22.2 on
+constexpr float kBinsPerUnit = (kHist - 2) / kRange;
+
+struct Fast {
+    unsigned long long hist[kWaves][kHist];
+    uint32_t key[kList];
+    uint32_t idx[kList];
+    unsigned long long sub[kThreads];
+    uint32_t few_key[kFew];
+    uint32_t few_idx[kFew];
+    uint32_t few_w[kFew];
+    unsigned long long range[kWaves];
+    uint64_t scan[2 * kWaves];
+    float red[2 * kWaves];
+    uint32_t n;
+    uint32_t lo, hi;
+    uint64_t all, sum;
+    int pick;
+};
+
+union Lds {
+    Shared any;
+    Fast fast;
+    __device__ Lds() {}
+};
+
+template <bool BF16>
+struct Groups {
+    static constexpr int kVec = BF16 ? 8 : 4;
+    const char* base;                        // 16-byte aligned, at or before the row's start
+    int off;                                 // elements between them
+    int V;
+    int n;                                   // groups
+    int run;                                 // groups of a wave, a multiple of 64
+
+    __device__ Groups(const void* logits, int v)
+    {
+        const uintptr_t a = reinterpret_cast<uintptr_t>(logits);
+        base = reinterpret_cast<const char*>(a & ~(uintptr_t)15);
+        off = (int)(a & 15) / (BF16 ? 2 : 4);
+        V = v;
+        n = (v + off + kVec - 1) / kVec;
+        run = ((n + kWaves - 1) / kWaves + 63) / 64 * 64;
+    }
+
+    __device__ int first(int group) const { return group * kVec - off; }
+
+    // The group's logits; columns outside the row (never read) and NaN as -inf.
+    __device__ void load(int group, float (&l)[kVec]) const
+    {
+        const int i0 = first(group);
+        if (i0 >= 0 && i0 + kVec <= V) {
+            const u32x4 v = *(const global_u32x4*)(base + (int64_t)group * 16);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                if constexpr (BF16) {
+                    l[2 * e] = __builtin_bit_cast(float, v[e] << 16);
+                    l[2 * e + 1] = __builtin_bit_cast(float, v[e] & 0xFFFF0000u);
+                } else {
+                    const uint32_t b = v[e];
+                    l[e] = __builtin_bit_cast(float, b);
+                }
+            }
+        } else {
+#pragma unroll
+            for (int e = 0; e < kVec; ++e) {
+                l[e] = -INFINITY;
+                if (i0 + e >= 0 && i0 + e < V) {
+                    if constexpr (BF16)
+                        l[e] = bf16_bits_to_f32(reinterpret_cast<const uint16_t*>(base)[(int64_t)group * kVec + e]);
+                    else
+                        l[e] = reinterpret_cast<const float*>(base)[(int64_t)group * kVec + e];
+                }
+            }
+        }
+#pragma unroll
+        for (int e = 0; e < kVec; ++e)
+            l[e] = l[e] != l[e] ? -INFINITY : l[e] + 0.0f;
+    }
+};
+
+// Weight of a logit where the maximum and the inverse temperature are finite.
+__device__ __forceinline__ uint32_t weight_finite(const Row& r, float l)
+{
+    return __float2uint_rn(expf((l - r.lmax) * r.inv_t) * kOne);
+}
+
+// Bin of a logit: 0 at the maximum, rising as it falls; kHist - 1 for what
+// surely has no weight.  Monotonous, being rounded products and differences.
+__device__ __forceinline__ int weight_bin(const Row& r, float l)
+{
+    return (int)fminf((r.lmax - l) * r.inv_t * kBinsPerUnit, (float)(kHist - 1));
+}
+
+__device__ __forceinline__ float block_reduce_max(float v, float* buf)
+{
+#pragma unroll
+    for (int d = 1; d < 64; d <<= 1)
+        v = fmaxf(v, __shfl_xor(v, d));
+    __syncthreads();
+    if ((threadIdx.x & 63) == 0)
+        buf[threadIdx.x >> 6] = v;
+    __syncthreads();
+    v = buf[0];
+#pragma unroll
+    for (int i = 1; i < kWaves; ++i)
+        v = fmaxf(v, buf[i]);
+    return v;
+}
+
+__device__ __forceinline__ uint64_t block_sum(uint64_t v, uint64_t* buf)
+{
+#pragma unroll
+    for (int d = 1; d < 64; d <<= 1)
+        v += __shfl_xor((unsigned long long)v, d);
+    __syncthreads();
+    if ((threadIdx.x & 63) == 0)
+        buf[threadIdx.x >> 6] = v;
+    __syncthreads();
+    v = 0;
+#pragma unroll
+    for (int i = 0; i < kWaves; ++i)
+        v += buf[i];
+    return v;
+}
+
+__device__ __forceinline__ bool comes_before(uint32_t ka, uint32_t ia, uint32_t kb, uint32_t ib)
+{
+    return ka > kb || (ka == kb && ia < ib);
+}
+
+// The few elements s.few_* [0, n): 1024 / size threads stand for each.  For this
+// thread's element sums f over the others j, threads of an element sharing them.
+template <class F>
+__device__ __forceinline__ void over_few(int n, F f)
+{
+    int share = kThreads;
+    while (share > 1 && (kThreads / share) < n)
+        share >>= 1;
+    const int part = threadIdx.x % share;
+    for (int j = part; j < n; j += share)
+        f(j);
+}
+
+__device__ __forceinline__ int few_share(int n)
+{
+    int share = kThreads;
+    while (share > 1 && (kThreads / share) < n)
+        share >>= 1;
+    return share;
+}
+
+// Sum over the `share` neighbouring threads that stand for one element.
+__device__ __forceinline__ uint64_t share_sum(uint64_t v, int share, uint64_t* wide)
+{
+    for (int d = 1; d < min(share, 64); d <<= 1)
+        v += __shfl_xor((unsigned long long)v, d);
+    if (share > 64) {                        // uniform: few elements, several waves each
+        __syncthreads();
+        if ((threadIdx.x & 63) == 0)
+            wide[threadIdx.x >> 6] = v;
+        __syncthreads();
+        const int waves = share >> 6, first = (threadIdx.x >> 6) / waves * waves;
+        v = 0;
+        for (int i = 0; i < waves; ++i)
+            v += wide[first + i];
+    }
+    return v;
+}
+
+// Top-k rows: the k-th largest of the threads' own maxima bounds the k-th
+// largest logit from below, and few logits lie above it.  Those are gathered
+// and compared with one another.  False if they are too many.
+template <bool BF16>
+__device__ bool sample_top_k(const SampleParams& p, const Settings& c, const Row& r, const Groups<BF16>& G, Fast& s,
+                             int64_t row, float mine)
+{
+    constexpr int kVec = Groups<BF16>::kVec;
+    // bins over the maxima's range; a thread without logits has none
+    const float lowest = -block_reduce_max(mine == -INFINITY ? -INFINITY : -mine, s.red);
+    if (!(r.lmax - lowest < INFINITY))
+        return false;
+    const float per = lowest < r.lmax ? (kThreads - 1) / (r.lmax - lowest) : 0.0f;
+    auto bin = [&](float l) { return (int)fminf((r.lmax - l) * per, (float)kThreads); };
+    uint32_t* count = reinterpret_cast<uint32_t*>(s.sub);
+    count[threadIdx.x] = 0;
     if (threadIdx.x == 0) {
-        p.tokens[row] = token;
-        if (p.logprobs)
-            p.logprobs[row] = logf((float)((double)kept(token) / (double)total));
+        s.n = 0;
+        s.pick = kThreads - 1;               // fewer maxima than k: every bin
+    }
+    __syncthreads();
+    if (mine != -INFINITY)
+        atomicAdd(&count[min(bin(mine), kThreads - 1)], 1u);
+    __syncthreads();
+    const uint64_t own = count[threadIdx.x];
+    const uint64_t upto = block_scan(own, s.scan);
+    const bool enough = upto >= (uint64_t)c.k && upto - own < (uint64_t)c.k;
+    if (enough)
+        s.pick = threadIdx.x;
+    __syncthreads();
+    const int last_bin = s.pick;
+    // with fewer than k maxima the k-th logit may lie below all of them
+    const bool all = block_sum(own, s.scan) < (uint64_t)c.k;
+    const int begin = (threadIdx.x >> 6) * G.run, end = min(G.n, begin + G.run);
+    for (int g = begin + (threadIdx.x & 63); g < end; g += 64) {
+        float l[kVec];
+        G.load(g, l);
+#pragma unroll
+        for (int e = 0; e < kVec; ++e) {
+            if (l[e] != -INFINITY && (all || bin(l[e]) <= last_bin)) {
+                const uint32_t at = atomicAdd(&s.n, 1u);
+                if (at < kFew) {
+                    s.few_key[at] = order_key(l[e]);
+                    s.few_idx[at] = (uint32_t)(G.first(g) + e);
+                    s.few_w[at] = weight_finite(r, l[e]);
+                }
+            }
+        }
+    }
+    __syncthreads();
+    const int n = (int)s.n;
+    if (n > kFew)
+        return false;
+    const int share = few_share(n), me = threadIdx.x / share;
+    const uint32_t key = me < n ? s.few_key[me] : 0, idx = me < n ? s.few_idx[me] : 0, w = me < n ? s.few_w[me] : 0;
+    uint64_t rank = 0, before = 0;
+    if (me < n)
+        over_few(n, [&](int j) {
+            if (comes_before(s.few_key[j], s.few_idx[j], key, idx)) {
+                ++rank;
+                before += s.few_w[j];
+            }
+        });
+    rank = share_sum(rank, share, s.scan);
+    __syncthreads();
+    before = share_sum(before, share, s.scan);
+    const bool lead = me < n && threadIdx.x % share == 0;
+    uint64_t total = block_sum(lead && rank < (uint64_t)c.k ? w : 0, s.scan);
+    const bool keep = me < n && rank < (uint64_t)c.k && w >= max(c.floor_w, 1u) &&
+                      (c.top_p >= 1.0f || before < top_p_mass(c.top_p, total));
+    total = block_sum(lead && keep ? w : 0, s.scan);
+    if (lead)
+        s.few_w[me] = keep ? w : 0;
+    __syncthreads();
+    uint64_t below = 0;                      // kept weight at lower indices
+    if (keep)
+        over_few(n, [&](int j) { below += s.few_idx[j] < idx ? s.few_w[j] : 0u; });
+    below = share_sum(below, share, s.scan);
+    const uint64_t t = target(c.u, total);
+    if (lead && keep && below <= t && t < below + w)
+        answer(p, row, (int)idx, w, total);
+    return true;
+}
+
+// The other rows: a histogram of the weights for each wave's range of indices
+// gives the row's weight and the bin where top-p (and min-p) cuts; only that
+// bin's elements are looked at one by one.  False if they are too many.
+template <bool BF16>
+__device__ bool sample_mass(const SampleParams& p, const Settings& c, const Row& r, const Groups<BF16>& G, Fast& s,
+                            int64_t row)
+{
+    constexpr int kVec = Groups<BF16>::kVec;
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+    const int begin = wave * G.run, end = min(G.n, begin + G.run);
+    const bool cut = c.top_p < 1.0f || c.floor_w > 0;
+    // the kept prefix ends with (key, last); floor_w applies on top
+    uint32_t key = 0, last = 0xFFFFFFFFu;
+    uint64_t total = 0;
+    if (!cut) {
+        uint64_t sum = 0;
+        for (int g = begin + lane; g < end; g += 64) {
+            float l[kVec];
+            G.load(g, l);
+#pragma unroll
+            for (int e = 0; e < kVec; ++e)
+                sum += weight_finite(r, l[e]);
+        }
+#pragma unroll
+        for (int d = 1; d < 64; d <<= 1)
+            sum += __shfl_xor((unsigned long long)sum, d);
+        if (lane == 0)
+            s.range[wave] = sum;
+        __syncthreads();
+    } else {
+        for (int i = lane; i < kHist; i += 64)
+            s.hist[wave][i] = 0;
+        if (threadIdx.x == 0) {
+            s.n = 0;
+            s.lo = 0xFFFFFFFFu;
+            s.hi = 0;
+        }
+        for (int g = begin + lane; g < end; g += 64) {
+            float l[kVec];
+            G.load(g, l);
+#pragma unroll
+            for (int e = 0; e < kVec; ++e) {
+                const uint32_t w = weight_finite(r, l[e]);
+                if (w)
+                    atomicAdd(&s.hist[wave][weight_bin(r, l[e])], (unsigned long long)w);
+            }
+        }
+        __syncthreads();
+        // the bin where top-p cuts
+        uint64_t own = 0;
+        if (threadIdx.x < kHist)
+#pragma unroll
+            for (int i = 0; i < kWaves; ++i)
+                own += s.hist[i][threadIdx.x];
+        const uint64_t upto = block_scan(own, s.scan);
+        if (threadIdx.x == kThreads - 1)
+            s.all = upto;
+        __syncthreads();
+        const uint64_t all = s.all;
+        const uint64_t mass = c.top_p < 1.0f ? top_p_mass(c.top_p, all) : all;
+        if (upto >= mass && upto - own < mass) {
+            s.pick = threadIdx.x;
+            s.sum = upto - own;
+        }
+        __syncthreads();
+        // the bins that are looked at one by one: that one, and where min-p cuts
+        // the one of its logarithm with a neighbour on both sides (rounding)
+        const int pick = s.pick;
+        const uint64_t pick_before = s.sum;
+        int from = pick, to = pick;
+        if (c.floor_w) {
+            // w >= floor_w from 2^31 exp(-z) >= floor_w - 1/2 on
+            const int f = (int)fminf(-logf(((float)c.floor_w - 0.5f) / kOne) * kBinsPerUnit, (float)(kHist - 1));
+            if (pick >= f - 1) {
+                from = max(min(pick, f - 1), 0);
+                to = min(pick, f + 1);
+            }
+        }
+        // bins below `from` are kept whole, bins above `to` not at all
+        for (int g = begin + lane; g < end; g += 64) {
+            float l[kVec];
+            G.load(g, l);
+#pragma unroll
+            for (int e = 0; e < kVec; ++e) {
+                const int b = weight_bin(r, l[e]);
+                if (b >= from && b <= to && l[e] != -INFINITY) {
+                    const uint32_t at = atomicAdd(&s.n, 1u);
+                    if (at < kList) {
+                        s.key[at] = order_key(l[e]);
+                        s.idx[at] = (uint32_t)(G.first(g) + e);
+                    }
+                }
+            }
+        }
+        __syncthreads();
+        const int n = (int)s.n;
+        if (n > kList)
+            return false;
+        auto weight_of = [&](uint32_t k) {
+            const uint32_t b = k ^ ((k >> 31) ? 0x80000000u : 0xFFFFFFFFu);
+            return weight_finite(r, __builtin_bit_cast(float, b));
+        };
+        if (c.top_p < 1.0f && pick <= to) {
+            // where in its bin: sub-bins over the bin's keys
+            for (int i = threadIdx.x; i < n; i += kThreads) {
+                const uint32_t b = s.key[i] ^ ((s.key[i] >> 31) ? 0x80000000u : 0xFFFFFFFFu);
+                if (weight_bin(r, __builtin_bit_cast(float, b)) == pick) {
+                    atomicMin(&s.lo, s.key[i]);
+                    atomicMax(&s.hi, s.key[i]);
+                }
+            }
+            s.sub[threadIdx.x] = 0;
+            __syncthreads();
+            const uint32_t lo = s.lo, hi = s.hi;
+            const int shift = max(0, 22 - (int)__clz((int)(hi - lo)));     // (hi - lo) >> shift < 1024
+            for (int i = threadIdx.x; i < n; i += kThreads) {
+                const uint32_t k = s.key[i];
+                if (k >= lo && k <= hi)
+                    atomicAdd(&s.sub[(hi - k) >> shift], (unsigned long long)weight_of(k));
+            }
+            __syncthreads();
+            if (threadIdx.x == 0)
+                s.n = 0;
+            const uint64_t o = s.sub[threadIdx.x];
+            const uint64_t up = block_scan(o, s.scan) + pick_before;
+            if (up >= mass && up - o < mass) {
+                s.pick = threadIdx.x;
+                s.sum = up - o;
+            }
+            __syncthreads();
+            const int sub = s.pick;
+            const uint64_t sub_before = s.sum;
+            for (int i = threadIdx.x; i < n; i += kThreads) {
+                const uint32_t k = s.key[i];
+                if (k >= lo && k <= hi && (int)((hi - k) >> shift) == sub) {
+                    const uint32_t at = atomicAdd(&s.n, 1u);
+                    if (at < kFew) {
+                        s.few_key[at] = k;
+                        s.few_idx[at] = s.idx[i];
+                        s.few_w[at] = weight_of(k);
+                    }
+                }
+            }
+            __syncthreads();
+            const int m = (int)s.n;
+            if (m > kFew)
+                return false;
+            const int share = few_share(m), me = threadIdx.x / share;
+            uint64_t before = 0;
+            if (me < m)
+                over_few(m, [&](int j) {
+                    if (comes_before(s.few_key[j], s.few_idx[j], s.few_key[me], s.few_idx[me]))
+                        before += s.few_w[j];
+                });
+            before = share_sum(before, share, s.scan) + sub_before;
+            // the last one kept: its predecessors stay below the mass, with it they reach it
+            if (me < m && threadIdx.x % share == 0 && before < mass && before + s.few_w[me] >= mass) {
+                s.lo = s.few_key[me];
+                s.hi = s.few_idx[me];
+            }
+            __syncthreads();
+            key = s.lo;
+            last = s.hi;
+        }
+        // kept weight of each range of indices
+        if (threadIdx.x < kWaves)
+            s.range[threadIdx.x] = 0;
+        __syncthreads();
+        {
+            uint64_t sum = 0;
+            for (int i = lane; i < from; i += 64)
+                sum += s.hist[wave][i];
+            if (sum)
+                atomicAdd(&s.range[wave], (unsigned long long)sum);
+        }
+        for (int i = threadIdx.x; i < n; i += kThreads) {
+            const uint32_t k = s.key[i], w = weight_of(k);
+            if (w >= c.floor_w && (k > key || (k == key && s.idx[i] <= last)))
+                atomicAdd(&s.range[((int)s.idx[i] + G.off) / kVec / G.run], (unsigned long long)w);
+        }
+        __syncthreads();
+    }
+    // the range the number falls into, then the place in it
+#pragma unroll
+    for (int i = 0; i < kWaves; ++i)
+        total += s.range[i];
+    const uint64_t t = target(c.u, total);
+    uint64_t before = 0;
+    int range = 0;
+    for (; range < kWaves - 1; ++range) {
+        if (before + s.range[range] > t)
+            break;
+        before += s.range[range];
+    }
+    const int per = (G.run + kThreads - 1) / kThreads;
+    const int first = range * G.run + threadIdx.x * per;
+    const int stop = min(min(first + per, (range + 1) * G.run), G.n);
+    auto kept = [&](float l, int i) -> uint32_t {
+        const uint32_t k = order_key(l), w = weight_finite(r, l);
+        return w >= c.floor_w && (k > key || (k == key && (uint32_t)i <= last)) ? w : 0u;
+    };
+    uint64_t own = 0;
+    for (int g = first; g < stop; ++g) {
+        float l[kVec];
+        G.load(g, l);
+#pragma unroll
+        for (int e = 0; e < kVec; ++e)
+            own += kept(l[e], G.first(g) + e);
+    }
+    uint64_t at = block_scan(own, s.scan) - own + before;
+    if (at <= t && t < at + own) {
+        for (int g = first; g < stop; ++g) {
+            float l[kVec];
+            G.load(g, l);
+#pragma unroll
+            for (int e = 0; e < kVec; ++e) {
+                const uint32_t w = kept(l[e], G.first(g) + e);
+                if (at <= t && t < at + w)
+                    answer(p, row, G.first(g) + e, w, total);
+                at += w;
+            }
+        }
+    }
+    return true;
+}
+
+template <bool BF16>
+__global__ void __launch_bounds__(kThreads) k_sample(SampleParams p)
+{
+    __shared__ Lds lds;
+    Fast& s = lds.fast;
+    const int64_t row = blockIdx.x;
+    Row r;
+    r.bf16 = BF16;
+    r.V = p.V;
+    r.logits = static_cast<const char*>(p.logits) + row * p.ld * (BF16 ? 2 : 4);
+    const float T = p.temperature ? p.temperature[row] : 1.0f;
+    const bool greedy = !(T > 0.0f);
+    r.inv_t = greedy ? 1.0f : 1.0f / T;
+    Settings c;
+    c.k = greedy ? 1 : (p.top_k ? p.top_k[row] : 0);
+    c.k = c.k > 0 && c.k < p.V ? c.k : 0;
+    c.top_p = greedy || !p.top_p ? 1.0f : fminf(p.top_p[row], 1.0f);       // NaN: 1
+    const float min_p = greedy || !p.min_p ? 0.0f : p.min_p[row];
+    c.floor_w = min_p > 0.0f ? (uint32_t)fmin(ceil((double)min_p * (double)kOne), (double)kOne) : 0u;
+    c.u = p.u[row];
+
+    const Groups<BF16> G(r.logits, r.V);
+    float mine = -INFINITY;
+    {
+        const int begin = (threadIdx.x >> 6) * G.run, end = min(G.n, begin + G.run);
+        for (int g = begin + (threadIdx.x & 63); g < end; g += 64) {
+            float l[Groups<BF16>::kVec];
+            G.load(g, l);
+#pragma unroll
+            for (int e = 0; e < Groups<BF16>::kVec; ++e)
+                mine = fmaxf(mine, l[e]);
+        }
+    }
+    r.lmax = block_reduce_max(mine, s.red);
+    if (r.lmax == -INFINITY) {               // every logit masked
+        if (threadIdx.x == 0) {
+            p.tokens[row] = -1;
+            if (p.logprobs)
+                p.logprobs[row] = -INFINITY;
+        }
+        return;
+    }
+    const bool finite = r.lmax < INFINITY && r.inv_t > 0.0f && r.inv_t < INFINITY;
+    bool done = false;
+    if (finite && c.k > 0 && c.k <= kThreads)
+        done = sample_top_k<BF16>(p, c, r, G, s, row, mine);
+    else if (finite && c.k == 0)
+        done = sample_mass<BF16>(p, c, r, G, s, row);
+    if (!done) {
+        __syncthreads();
+        sample_any(p, c, r, lds.any, row);
     }
 }
 
@@ -348,7 +875,10 @@ __global__ void __launch_bounds__(kThreads) k_sample(SampleParams p, bool bf16)
 
 hipError_t launch_sample(const SampleParams& p, bool bf16, hipStream_t st)
 {
-    hipLaunchKernelGGL(k_sample, dim3((unsigned)p.B), dim3(kThreads), 0, st, p, bf16);
+    if (bf16)
+        hipLaunchKernelGGL(k_sample<true>, dim3((unsigned)p.B), dim3(kThreads), 0, st, p);
+    else
+        hipLaunchKernelGGL(k_sample<false>, dim3((unsigned)p.B), dim3(kThreads), 0, st, p);
     return hipGetLastError();
 }
 
