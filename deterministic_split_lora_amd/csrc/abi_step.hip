@@ -12,6 +12,7 @@ namespace {
 constexpr int64_t kMaxDim = (int64_t{1} << 31) - 1;
 constexpr int64_t kMaxGrid = (int64_t{1} << 31) - 1;
 constexpr int64_t kMaxGridY = 65535;
+constexpr int64_t kMaxPitch = int64_t{1} << 25;        // bytes; 64 rows stay below 2^32
 constexpr int64_t kMaxVocabulary = int64_t{1} << 22;   // a row's weight stays below 2^53
 
 bool aligned(const void* p, unsigned n)
@@ -29,6 +30,8 @@ int check_mx4(const uint8_t* q, int64_t ld_q, const uint8_t* s, int64_t ld_s, in
 {
     if (ld_q < K / 2 || ld_s < K / kMxBlock)
         return LORA_ERR_SHAPE;
+    if (ld_q > kMaxPitch)
+        return LORA_ERR_UNSUPPORTED;
     if (!aligned(q, 16) || ld_q % 16 || !aligned(s, 4) || ld_s % 4)
         return LORA_ERR_ALIGN;
     return LORA_OK;
@@ -100,6 +103,8 @@ int linear(const void* x, int64_t ld_x, const uint8_t* xs, int64_t ld_xs, const 
         return LORA_ERR_NULL;
     if (ld_y < N || (!x_is_mx4 && ld_x < K))
         return LORA_ERR_SHAPE;
+    if ((!x_is_mx4 && ld_x > kMaxPitch / 2) || ld_ws > kMaxPitch || ld_xs > kMaxPitch)
+        return LORA_ERR_UNSUPPORTED;
     if (x_is_mx4 && (st = check_mx4(static_cast<const uint8_t*>(x), ld_x, xs, ld_xs, K)) != LORA_OK)
         return st;
     if ((st = check_mx4(wq, ld_wq, ws, ld_ws, K)) != LORA_OK)

@@ -12,12 +12,11 @@ typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
 typedef int32_t i32x8 __attribute__((ext_vector_type(8)));
 typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
 
-// The scale 2^(b-127) as the fp32 operand of the conversion instructions
-// (2^-127, b = 0, is below the smallest normal fp32; b = 255 gives a NaN).
+// The scale 2^(b-127) as the fp32 operand of the conversion instructions, which
+// take its exponent field alone (so 0 stands for 2^-127 and 255 for NaN).
 __device__ __forceinline__ float mx_scale_f32(uint32_t b)
 {
-    const uint32_t bits = b == 0 ? 0x00400000u : (b == 255 ? 0x7FC00000u : b << 23);
-    return __builtin_bit_cast(float, bits);
+    return __builtin_bit_cast(float, b << 23);
 }
 
 // Eight codes (one 32-bit word) as bf16, times the scale.  Exact: a code has two

@@ -2,15 +2,14 @@
 //
 // Arithmetic, the same in every kernel of this file so that schedules agree
 // bit for bit.  K is cut into split_k chunks.  A chunk's sum is one chain of
-// matrix-core steps over its blocks in ascending k, four blocks (128 k) at a
-// time, from zero, in fp32; block g of the four belongs to the lanes of group g
-// (li = lane % 16, g = lane / 16).  Chunk sums are added in ascending order and
-// the total is rounded once to bf16.  Blocks past the chunk's end enter as
-// zeros.
-//   bf16 x: a step is four V_MFMA_F32_16X16X32_BF16; the s-th takes elements
-//     8s .. 8s+7 of each block, the codes converted to bf16 (exactly) on the way.
-//   MX4 x: a step is one V_MFMA_SCALE_F32_16X16X128_F8F6F4, which takes both
-//     operands' codes and scales as they are stored.
+// matrix-core steps in ascending k, from zero, in fp32.  Chunk sums are added in
+// ascending order and the total is rounded once to bf16.
+//   bf16 x: a step is one V_MFMA_F32_16X16X32_BF16 over a block of 32, lane
+//     group g (li = lane % 16, g = lane / 16) holding elements 8g .. 8g+7 of it;
+//     W's codes are converted to bf16 (exactly) on the way.
+//   MX4 x: a step is one V_MFMA_SCALE_F32_16X16X128_F8F6F4 over four blocks, lane
+//     group g holding block g; both operands' codes and scales enter as they are
+//     stored.  Blocks past the chunk's end enter as zeros.
 // The "row" operand is W, so a lane's accumulator holds four consecutive output
 // columns of one token.
 #include "mx4_tile.h"
@@ -19,27 +18,58 @@ namespace lora {
 
 namespace {
 
-constexpr int kStepK = 128;
+constexpr int kStepK = 128;                  // k of one step's loads
+constexpr int kScaleSteps = 16;              // steps whose scales are loaded together
 
-__device__ __forceinline__ MxOperand load_mx(const uint8_t* q, const uint8_t* s, int64_t k, bool ok)
+__device__ __forceinline__ MxOperand mx_operand(u32x4 q, uint32_t s, bool ok)
 {
-    MxOperand o;
-    o.q = ok ? *(const global_u32x4*)(q + k / 2) : u32x4{0, 0, 0, 0};
-    o.s = ok ? s[k / kMxBlock] : 127u;
-    return o;
+    return ok ? MxOperand{q, s} : MxOperand{u32x4{0, 0, 0, 0}, 127};
+}
+
+// Four words at a word-aligned address.
+typedef uint32_t u32x4_word_aligned __attribute__((ext_vector_type(4), aligned(4)));
+
+// A wave-uniform base and a lane's 32-bit offset from it.
+template <class T>
+__device__ __forceinline__ T load_at(const uint8_t* base, uint32_t offset)
+{
+    typedef __attribute__((address_space(1))) const uint8_t global_u8;
+    typedef __attribute__((address_space(1))) const T global_t;
+    return *(global_t*)((global_u8*)base + offset);
+}
+
+// Codes of block g in lane group g, element pairs 4d .. 4d+3 in word d, to the
+// words of block s in q[s], lane group g holding word g: a 4 x 4 transpose of
+// (lane group, word).
+__device__ __forceinline__ void transpose_groups(u32x4& q)
+{
+    uint32_t a = q[0], b = q[1], c = q[2], d = q[3];
+    const auto ac = __builtin_amdgcn_permlane32_swap(a, c, false, false);
+    const auto bd = __builtin_amdgcn_permlane32_swap(b, d, false, false);
+    const auto ab = __builtin_amdgcn_permlane16_swap(ac[0], bd[0], false, false);
+    const auto cd = __builtin_amdgcn_permlane16_swap(ac[1], bd[1], false, false);
+    q = u32x4{ab[0], ab[1], cd[0], cd[1]};
 }
 
 // Few tokens: a workgroup owns 16 RT tokens x 16 CT columns (times the column
-// groups G), its wave (g, s) the chain of chunk s; the chains meet in LDS.
-template <bool XMX, int RT, int CT>
-__global__ void __launch_bounds__(1024) k_mx4_linear_rows(Mx4LinearParams p, int groups)
+// groups), its wave (group, s) the chain of chunk s; the chains meet in LDS.
+// Bound by how many loads are in flight: W's come D steps of 128 k ahead, those
+// of x (which the other workgroups read too, so that it is near) DX ahead, and a
+// wave never meets the others before its chain is done.  Every load is 64
+// contiguous bytes a row: 16 bytes a lane, x of one block, W of four blocks, one a
+// lane group, whose words the lane groups then exchange (bf16 x).  So do the
+// scales, 64 blocks at a time, which a wave keeps in its part of LDS: read four
+// bytes a row and step they would come from L2 every time, a line each.
+template <bool XMX, int RT, int CT, int D, int DX, int THREADS>
+__global__ void __launch_bounds__(THREADS) k_mx4_linear_rows(Mx4LinearParams p, int groups)
 {
+    static_assert(D % DX == 0 && kScaleSteps % D == 0, "the rings turn together");
     extern __shared__ float lds[];
     const int lane = threadIdx.x & 63;
     const int li = lane & 15, g = lane >> 4;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int S = p.split_k;
-    const int chunk = wave % S, group = wave / S;
+    const int chunk = wave % S, group = wave / S;             // wave = group * S + chunk
     const int64_t n0 = ((int64_t)blockIdx.x * groups + group) * (16 * CT);
     const int64_t m0 = (int64_t)blockIdx.y * (16 * RT);
 
@@ -50,54 +80,162 @@ __global__ void __launch_bounds__(1024) k_mx4_linear_rows(Mx4LinearParams p, int
         for (int c = 0; c < CT; ++c)
             acc[r][c] = f32x4{0, 0, 0, 0};
 
-    const uint8_t* wq[CT];
-    const uint8_t* ws[CT];
+    const int64_t kc = (int64_t)chunk * p.k_chunk;
+    const int steps = (p.k_chunk + kStepK - 1) / kStepK, last = steps - 1;
+    const int rem = (p.k_chunk - last * kStepK) / kMxBlock;    // blocks of the last step
+    // in the last step a lane group without a block reads the step's first one
+    const uint32_t back = g < rem ? 0u : 16u * g;
+
+    // first row of the tiles (a group past the last column repeats the last row)
+    const int64_t nb = min(n0, p.N - 1);
+    const uint8_t* wq0 = p.wq + nb * p.ld_wq + kc / 2;
+    const uint8_t* ws0 = p.ws + nb * p.ld_ws;
+    const uint8_t* xq0 = static_cast<const uint8_t*>(p.x) + (XMX ? m0 * p.ld_x + kc / 2 : 2 * (m0 * p.ld_x + kc));
+    const uint8_t* xs0 = XMX ? p.xs + m0 * p.ld_xs : nullptr;
+    const int sb0 = (int)(kc / kMxBlock);                      // the chunk's first scale byte
+    const int last_word = (p.k_chunk / kMxBlock * S - 1) >> 2;
+    uint32_t wo[CT], wso[CT], xo[RT], xso[RT];
 #pragma unroll
     for (int c = 0; c < CT; ++c) {
-        const int64_t n = min(n0 + 16 * c + li, p.N - 1);
-        wq[c] = p.wq + n * p.ld_wq;
-        ws[c] = p.ws + n * p.ld_ws;
+        const int64_t n = min(nb + 16 * c + li, p.N - 1) - nb;
+        wo[c] = (uint32_t)(n * p.ld_wq) + 16 * g;
+        wso[c] = (uint32_t)(n * p.ld_ws);
     }
-    const uint8_t* xq[RT];
-    const uint8_t* xs[RT];
 #pragma unroll
     for (int r = 0; r < RT; ++r) {
-        const int64_t m = min(m0 + 16 * r + li, p.M - 1);
-        xq[r] = static_cast<const uint8_t*>(p.x) + m * p.ld_x * (XMX ? 1 : 2);
-        xs[r] = XMX ? p.xs + m * p.ld_xs : nullptr;
+        const int64_t m = min(m0 + 16 * r + li, p.M - 1) - m0;
+        xo[r] = (uint32_t)(m * p.ld_x) * (XMX ? 1 : 2) + 16 * g;
+        xso[r] = XMX ? (uint32_t)(m * p.ld_xs) : 0;
     }
-    const int64_t kc = (int64_t)chunk * p.k_chunk;
-    for (int t = 0; t < p.k_chunk; t += kStepK) {
-        const bool ok = t + g * kMxBlock < p.k_chunk;
-        const int64_t k = kc + t + g * kMxBlock;
-        MxOperand w[CT];
+
+    u32x4 w[D][CT], x[DX][RT][XMX ? 1 : 4];
+
+    // This wave's scales, W's tiles first: [tile][16 rows][kScaleSteps words], a
+    // word the four blocks of a step.
+    constexpr int kTile = 256, kScaleTiles = CT + (XMX ? RT : 0);
+    constexpr int kWaveLds = (RT * CT > kScaleTiles ? RT * CT : kScaleTiles) * kTile;
+    uint32_t* sc = reinterpret_cast<uint32_t*>(lds) + wave * kWaveLds;
+    const int shift = 8 * (sb0 & 3);
+    auto stage_scales = [&](int j) {
+        // lane group g has words 4g .. 4g+3 of the rows, if there are so many steps
+        if (j + 4 * g >= steps)
+            return;
+        const int word = ((sb0 + 4 * j) >> 2) + 4 * g;
+        const bool inside = word + 4 <= last_word;
+        uint32_t v[kScaleTiles][5];
+#pragma unroll
+        for (int i = 0; i < kScaleTiles; ++i) {
+            const uint8_t* s0 = i < CT ? ws0 : xs0;
+            const uint32_t off = i < CT ? wso[i < CT ? i : 0] : xso[i < CT ? 0 : i - CT];
+            if (inside) {
+                const u32x4 q = load_at<u32x4_word_aligned>(s0, off + 4 * word);
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                    v[i][e] = q[e];
+                v[i][4] = shift ? load_at<uint32_t>(s0, off + 4 * word + 16) : 0;
+            } else {
+#pragma unroll
+                for (int e = 0; e < 5; ++e)
+                    v[i][e] = load_at<uint32_t>(s0, off + 4 * min(word + e, last_word));
+            }
+        }
+#pragma unroll
+        for (int i = 0; i < kScaleTiles; ++i) {
+            u32x4 q;
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+                q[e] = __builtin_amdgcn_alignbit(v[i][e + 1], v[i][e], shift);
+            *reinterpret_cast<u32x4*>(sc + i * kTile + li * kScaleSteps + 4 * g) = q;
+        }
+    };
+    auto load_w = [&](u32x4 (&b)[CT], int j) {
+        const uint32_t less = j == last ? back : 0;
 #pragma unroll
         for (int c = 0; c < CT; ++c)
-            w[c] = load_mx(wq[c], ws[c], k, ok);
+            b[c] = load_at<u32x4>(wq0 + j * 64, wo[c] - less);
+    };
+    auto load_x = [&](u32x4 (&b)[RT][XMX ? 1 : 4], int j) {
+        const uint32_t less = j == last ? back : 0;
 #pragma unroll
         for (int r = 0; r < RT; ++r) {
             if constexpr (XMX) {
-                const MxOperand x = load_mx(xq[r], xs[r], k, ok);
-#pragma unroll
-                for (int c = 0; c < CT; ++c)
-                    acc[r][c] = mfma_mx4(w[c], x, acc[r][c]);
+                b[r][0] = load_at<u32x4>(xq0 + j * 64, xo[r] - less);
             } else {
 #pragma unroll
-                for (int s = 0; s < 4; ++s) {
-                    const bf16x8 x = ok ? load_bf16x8(reinterpret_cast<const uint16_t*>(xq[r]) + k + 8 * s)
-                                        : bf16x8_zero();
+                for (int s = 0; s < 4; ++s)
+                    b[r][s] = load_at<u32x4>(xq0 + j * 256 + (j < last || s < rem ? 64 * s : 0), xo[r]);
+            }
+        }
+    };
+    auto scales = [&](int tile, int j) { return sc[tile * kTile + li * kScaleSteps + j % kScaleSteps]; };
+    auto multiply = [&](u32x4 (&a)[CT], u32x4 (&b)[RT][XMX ? 1 : 4], int j) {
+        if constexpr (XMX) {
+            const bool ok = j < last || g < rem;
+            MxOperand wm[CT];
 #pragma unroll
-                    for (int c = 0; c < CT; ++c)
-                        acc[r][c] = mfma_16x16x32(mx4_to_bf16(w[c].q[s], mx_scale_f32(w[c].s)), x, acc[r][c]);
+            for (int c = 0; c < CT; ++c)
+                wm[c] = mx_operand(a[c], scales(c, j) >> (8 * g), ok);
+#pragma unroll
+            for (int r = 0; r < RT; ++r) {
+                const MxOperand xm = mx_operand(b[r][0], scales(CT + r, j) >> (8 * g), ok);
+#pragma unroll
+                for (int c = 0; c < CT; ++c)
+                    acc[r][c] = mfma_mx4(wm[c], xm, acc[r][c]);
+            }
+        } else {
+            uint32_t s4[CT];
+#pragma unroll
+            for (int c = 0; c < CT; ++c) {
+                transpose_groups(a[c]);
+                s4[c] = scales(c, j);
+            }
+#pragma unroll
+            for (int s = 0; s < 4; ++s) {
+                if (j == last && s >= rem)
+                    break;
+#pragma unroll
+                for (int c = 0; c < CT; ++c) {
+                    const bf16x8 wb = mx4_to_bf16(a[c][s], mx_scale_f32((s4[c] >> (8 * s)) & 255u));
+#pragma unroll
+                    for (int r = 0; r < RT; ++r)
+                        acc[r][c] = mfma_16x16x32(wb, __builtin_bit_cast(bf16x8, b[r][s]), acc[r][c]);
                 }
             }
         }
+    };
+
+    // loads past the last step repeat it, so that how many are in flight is
+    // known wherever one is waited for
+#pragma unroll
+    for (int d = 0; d < D; ++d) {
+        load_w(w[d], min(d, last));
+        if (d < DX)
+            load_x(x[d], min(d, last));
+    }
+    int j = 0;
+    for (; j + D < steps; j += D) {
+        if (j % kScaleSteps == 0)
+            stage_scales(j);
+#pragma unroll
+        for (int d = 0; d < D; ++d) {
+            multiply(w[d], x[d % DX], j + d);
+            load_w(w[d], min(j + D + d, last));
+            load_x(x[d % DX], min(j + DX + d, last));
+        }
+    }
+    if (j % kScaleSteps == 0)
+        stage_scales(j);
+#pragma unroll
+    for (int d = 0; d < D; ++d) {
+        if (j + d < steps)
+            multiply(w[d], x[d % DX], j + d);
+        if (d + DX < D)
+            load_x(x[d % DX], min(j + DX + d, last));
     }
 
     // chains to LDS: [group][chunk][r][c][lane][4], then a thread adds its
     // output's chunks in ascending order
-    constexpr int kTile = 256;
-    float* mine = lds + ((int64_t)group * S + chunk) * (RT * CT * kTile);
+    float* mine = lds + wave * kWaveLds;     // wave = group * S + chunk
 #pragma unroll
     for (int r = 0; r < RT; ++r)
 #pragma unroll
@@ -107,10 +245,10 @@ __global__ void __launch_bounds__(1024) k_mx4_linear_rows(Mx4LinearParams p, int
     const int quads = groups * RT * CT * 64;
     for (int i = threadIdx.x; i < quads; i += blockDim.x) {
         const int l = i & 63, tile = (i >> 6) % (RT * CT), grp = (i >> 6) / (RT * CT);
-        const float* src = lds + ((int64_t)grp * S * (RT * CT) + tile) * kTile + l * 4;
+        const float* src = lds + grp * S * kWaveLds + tile * kTile + l * 4;
         f32x4 sum = *reinterpret_cast<const f32x4*>(src);
         for (int s = 1; s < S; ++s) {
-            const f32x4 v = *reinterpret_cast<const f32x4*>(src + s * (RT * CT * kTile));
+            const f32x4 v = *reinterpret_cast<const f32x4*>(src + s * kWaveLds);
 #pragma unroll
             for (int e = 0; e < 4; ++e)
                 sum[e] += v[e];
@@ -125,14 +263,16 @@ __global__ void __launch_bounds__(1024) k_mx4_linear_rows(Mx4LinearParams p, int
     }
 }
 
-template <bool XMX, int RT, int CT>
+template <bool XMX, int RT, int CT, int D, int DX, int THREADS>
 hipError_t launch_rows(const Mx4LinearParams& p, hipStream_t st)
 {
     const int groups = p.split_k < 4 ? 4 / p.split_k : 1;
     const int64_t cols = 16 * CT * groups;
     const dim3 grid((unsigned)((p.N + cols - 1) / cols), (unsigned)((p.M + 16 * RT - 1) / (16 * RT)));
-    const size_t lds = (size_t)groups * p.split_k * RT * CT * 1024;
-    hipLaunchKernelGGL((k_mx4_linear_rows<XMX, RT, CT>), grid, dim3(64 * groups * p.split_k), lds, st, p, groups);
+    const int tiles = RT * CT > CT + (XMX ? RT : 0) ? RT * CT : CT + (XMX ? RT : 0);
+    const size_t lds = (size_t)groups * p.split_k * tiles * 1024;
+    hipLaunchKernelGGL((k_mx4_linear_rows<XMX, RT, CT, D, DX, THREADS>), grid, dim3(64 * groups * p.split_k), lds, st,
+                       p, groups);
     return hipGetLastError();
 }
 
@@ -151,11 +291,20 @@ hipError_t launch_mx4_linear(const Mx4LinearParams& p, bool x_is_mx4, hipStream_
             return x_is_mx4 ? launch_tile<true, 128, 256, true>(p, st) : launch_tile<false, 128, 256, true>(p, st);
         return x_is_mx4 ? launch_tile<true, 256, 256, false>(p, st) : launch_tile<false, 128, 256, false>(p, st);
     }
+    if (x_is_mx4) {
+        if (p.M <= 16)
+            return launch_rows<true, 1, 1, 8, 4, 1024>(p, st);
+        if (p.M <= 32)
+            return launch_rows<true, 2, 1, 4, 2, 1024>(p, st);
+        return launch_rows<true, 4, 1, 2, 2, 1024>(p, st);
+    }
     if (p.M <= 16)
-        return x_is_mx4 ? launch_rows<true, 1, 1>(p, st) : launch_rows<false, 1, 1>(p, st);
+        return launch_rows<false, 1, 1, 4, 2, 1024>(p, st);
     if (p.M <= 32)
-        return x_is_mx4 ? launch_rows<true, 2, 1>(p, st) : launch_rows<false, 2, 1>(p, st);
-    return x_is_mx4 ? launch_rows<true, 4, 1>(p, st) : launch_rows<false, 4, 1>(p, st);
+        return launch_rows<false, 2, 1, 4, 2, 1024>(p, st);
+    if (p.M <= 48)
+        return launch_rows<false, 3, 1, 4, 1, 1024>(p, st);
+    return launch_rows<false, 4, 1, 4, 1, 1024>(p, st);
 }
 
 }  // namespace lora

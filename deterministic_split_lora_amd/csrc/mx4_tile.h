@@ -199,53 +199,53 @@ __global__ void __launch_bounds__(kTileWaves * 64, 2) k_mx4_linear_tile(Mx4Linea
         const uint8_t* xs = lds + stage * T::kStage;
         const uint8_t* ws = xs + T::kXStage;
         const int left = p.k_chunk - t * 128;
-        const bool ok = g * kMxBlock < left;
-        const int block = (int)(k / kMxBlock) + g;
-        const uint8_t* sc = lds + T::kStages * T::kStage + ((block >> 2) % kSlots) * (T::kScaleRows * 4) + (block & 3);
+        // the scale of one block, of row 0 (rows are 4 bytes apart)
+        auto scale_bytes = [&](int block) {
+            return lds + T::kStages * T::kStage + ((block >> 2) % kSlots) * (T::kScaleRows * 4) + (block & 3);
+        };
 
-        MxOperand w[T::kCols];
-#pragma unroll
-        for (int c = 0; c < T::kCols; ++c) {
-            const int row = wn * (TN / 4) + 16 * c + li;
-            w[c].q = *reinterpret_cast<const u32x4*>(ws + row * 64 + ((g ^ swizzle4(row)) * 16));
-            w[c].s = sc[row * 4];
-            if (!ok) {
-                w[c].q = u32x4{0, 0, 0, 0};
-                w[c].s = 127;
-            }
-        }
         if constexpr (XMX) {
+            const bool ok = g * kMxBlock < left;
+            const int block = (int)(k / kMxBlock) + g;
+            const uint8_t* sc = scale_bytes(block);
+            MxOperand w[T::kCols];
+#pragma unroll
+            for (int c = 0; c < T::kCols; ++c) {
+                const int row = wn * (TN / 4) + 16 * c + li;
+                w[c].q = *reinterpret_cast<const u32x4*>(ws + row * 64 + ((g ^ swizzle4(row)) * 16));
+                w[c].s = sc[row * 4];
+                if (!ok)
+                    w[c] = MxOperand{u32x4{0, 0, 0, 0}, 127};
+            }
 #pragma unroll
             for (int r = 0; r < T::kRows; ++r) {
                 const int row = wm * (TM / 2) + 16 * r + li;
                 MxOperand x;
                 x.q = *reinterpret_cast<const u32x4*>(xs + row * 64 + ((g ^ swizzle4(row)) * 16));
                 x.s = sc[(TN + row) * 4];
-                if (!ok) {
-                    x.q = u32x4{0, 0, 0, 0};
-                    x.s = 127;
-                }
+                if (!ok)
+                    x = MxOperand{u32x4{0, 0, 0, 0}, 127};
 #pragma unroll
                 for (int c = 0; c < T::kCols; ++c)
                     acc[r][c] = mfma_mx4(w[c], x, acc[r][c]);
             }
         } else {
-            float scale[T::kCols];
-#pragma unroll
-            for (int c = 0; c < T::kCols; ++c)
-                scale[c] = mx_scale_f32(w[c].s);
 #pragma unroll
             for (int s = 0; s < 4; ++s) {
+                if (s * kMxBlock >= left)
+                    break;
+                const uint8_t* sc = scale_bytes((int)(k / kMxBlock) + s);
                 bf16x8 wb[T::kCols];
 #pragma unroll
-                for (int c = 0; c < T::kCols; ++c)
-                    wb[c] = mx4_to_bf16(w[c].q[s], scale[c]);
+                for (int c = 0; c < T::kCols; ++c) {
+                    const int row = wn * (TN / 4) + 16 * c + li;
+                    const uint32_t q = *reinterpret_cast<const uint32_t*>(ws + row * 64 + ((s ^ swizzle4(row)) * 16) + 4 * g);
+                    wb[c] = mx4_to_bf16(q, mx_scale_f32(sc[row * 4]));
+                }
 #pragma unroll
                 for (int r = 0; r < T::kRows; ++r) {
                     const int row = wm * (TM / 2) + 16 * r + li;
-                    u32x4 x = *reinterpret_cast<const u32x4*>(xs + row * 256 + (((4 * g + s) ^ swizzle16(row)) * 16));
-                    if (!ok)
-                        x = u32x4{0, 0, 0, 0};
+                    const u32x4 x = *reinterpret_cast<const u32x4*>(xs + row * 256 + (((4 * s + g) ^ swizzle16(row)) * 16));
 #pragma unroll
                     for (int c = 0; c < T::kCols; ++c)
                         acc[r][c] = mfma_16x16x32(wb[c], __builtin_bit_cast(bf16x8, x), acc[r][c]);
