@@ -12,7 +12,7 @@ namespace {
 constexpr int64_t kMaxDim = (int64_t{1} << 31) - 1;
 constexpr int64_t kMaxGrid = (int64_t{1} << 31) - 1;
 constexpr int64_t kMaxGridY = 65535;
-constexpr int64_t kMaxPitch = int64_t{1} << 25;        // bytes; 64 rows stay below 2^32
+constexpr int64_t kMaxPitch = int64_t{1} << 23;        // bytes; 256 rows stay below 2^32
 constexpr int64_t kMaxVocabulary = int64_t{1} << 22;   // a row's weight stays below 2^53
 
 bool aligned(const void* p, unsigned n)

@@ -58,4 +58,17 @@ __device__ __forceinline__ uint32_t bf16_to_mx4(u32x4 v, float scale)
     return __builtin_amdgcn_cvt_scalef32_pk_fp4_bf16(w, __builtin_bit_cast(bf16x2, v3), scale, 3);
 }
 
+// Codes of block g in lane group g, element pairs 4d .. 4d+3 in word d, to the
+// words of block s in q[s], lane group g holding word g: a 4 x 4 transpose of
+// (lane group, word).
+__device__ __forceinline__ void transpose_groups(u32x4& q)
+{
+    uint32_t a = q[0], b = q[1], c = q[2], d = q[3];
+    const auto ac = __builtin_amdgcn_permlane32_swap(a, c, false, false);
+    const auto bd = __builtin_amdgcn_permlane32_swap(b, d, false, false);
+    const auto ab = __builtin_amdgcn_permlane16_swap(ac[0], bd[0], false, false);
+    const auto cd = __builtin_amdgcn_permlane16_swap(ac[1], bd[1], false, false);
+    q = u32x4{ab[0], ab[1], cd[0], cd[1]};
+}
+
 }  // namespace lora

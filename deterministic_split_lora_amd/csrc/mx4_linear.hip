@@ -13,6 +13,7 @@
 // The "row" operand is W, so a lane's accumulator holds four consecutive output
 // columns of one token.
 #include "mx4_tile.h"
+#include <stdlib.h>
 
 namespace lora {
 
@@ -36,19 +37,6 @@ __device__ __forceinline__ T load_at(const uint8_t* base, uint32_t offset)
     typedef __attribute__((address_space(1))) const uint8_t global_u8;
     typedef __attribute__((address_space(1))) const T global_t;
     return *(global_t*)((global_u8*)base + offset);
-}
-
-// Codes of block g in lane group g, element pairs 4d .. 4d+3 in word d, to the
-// words of block s in q[s], lane group g holding word g: a 4 x 4 transpose of
-// (lane group, word).
-__device__ __forceinline__ void transpose_groups(u32x4& q)
-{
-    uint32_t a = q[0], b = q[1], c = q[2], d = q[3];
-    const auto ac = __builtin_amdgcn_permlane32_swap(a, c, false, false);
-    const auto bd = __builtin_amdgcn_permlane32_swap(b, d, false, false);
-    const auto ab = __builtin_amdgcn_permlane16_swap(ac[0], bd[0], false, false);
-    const auto cd = __builtin_amdgcn_permlane16_swap(ac[1], bd[1], false, false);
-    q = u32x4{ab[0], ab[1], cd[0], cd[1]};
 }
 
 // Few tokens: a workgroup owns 16 RT tokens x 16 CT columns (times the column
@@ -276,20 +264,80 @@ hipError_t launch_rows(const Mx4LinearParams& p, hipStream_t st)
     return hipGetLastError();
 }
 
+// Second launch of the split schedule: the chunks' sums, added in ascending
+// order, eight columns a thread.
+__global__ void __launch_bounds__(256) k_mx4_linear_join(Mx4LinearParams p)
+{
+    const int64_t per_row = p.N / 8, i = (int64_t)blockIdx.x * 256 + threadIdx.x;
+    const int64_t m = i / per_row, n = (i - m * per_row) * 8;
+    if (m >= p.M)
+        return;
+    const float* src = p.partial + m * p.N + n;
+    f32x4 a = *reinterpret_cast<const f32x4*>(src), b = *reinterpret_cast<const f32x4*>(src + 4);
+    for (int s = 1; s < p.split_k; ++s) {
+        src += p.M * p.N;
+        const f32x4 u = *reinterpret_cast<const f32x4*>(src), v = *reinterpret_cast<const f32x4*>(src + 4);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            a[e] += u[e];
+            b[e] += v[e];
+        }
+    }
+    u16x8 out;
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+        out[e] = f32_to_bf16_bits(a[e]);
+        out[4 + e] = f32_to_bf16_bits(b[e]);
+    }
+    *reinterpret_cast<u16x8*>(p.y + m * p.ld_y + n) = out;
+}
+
+template <bool XMX, int TM, int TN>
+hipError_t launch_split_tile(const Mx4LinearParams& p, hipStream_t st)
+{
+    const hipError_t e = launch_tile<XMX, TM, TN, kPartial>(p, st);
+    if (e != hipSuccess)
+        return e;
+    hipLaunchKernelGGL(k_mx4_linear_join, dim3((unsigned)((p.M * (p.N / 8) + 255) / 256)), dim3(256), 0, st, p);
+    return hipGetLastError();
+}
+
+// Which kernel a call takes.
+enum Schedule { kRows, kSplit64, kTile64, kTile128, kTile256 };
+
+Schedule schedule_for(int64_t M, int64_t N, int32_t k_chunk, int32_t split_k, bool x_is_mx4)
+{
+    if (const char* e = getenv("MX4_SCHED")) return (Schedule)atoi(e);  // EXPERIMENT
+    if (M <= 64)
+        return kRows;
+    return split_k > 1 || !x_is_mx4 ? kTile128 : kTile256;
+}
+
 }  // namespace
 
 int64_t mx4_linear_workspace(int64_t M, int64_t N, int32_t k_chunk, int32_t split_k, bool x_is_mx4)
 {
-    (void)M; (void)N; (void)k_chunk; (void)split_k; (void)x_is_mx4;
-    return 0;
+    return schedule_for(M, N, k_chunk, split_k, x_is_mx4) == kSplit64 ? M * N * split_k * (int64_t)sizeof(float) : 0;
 }
 
 hipError_t launch_mx4_linear(const Mx4LinearParams& p, bool x_is_mx4, hipStream_t st)
 {
-    if (p.M > 64 && p.k_chunk * (int64_t)p.split_k >= 512) {
-        if (p.split_k > 1)
-            return x_is_mx4 ? launch_tile<true, 128, 256, true>(p, st) : launch_tile<false, 128, 256, true>(p, st);
-        return x_is_mx4 ? launch_tile<true, 256, 256, false>(p, st) : launch_tile<false, 128, 256, false>(p, st);
+    const bool one = p.split_k == 1;
+    switch (schedule_for(p.M, p.N, p.k_chunk, p.split_k, x_is_mx4)) {
+    case kSplit64:
+        return x_is_mx4 ? launch_split_tile<true, 128, 128>(p, st) : launch_split_tile<false, 64, 128>(p, st);
+    case kTile64:
+        if (x_is_mx4)
+            return one ? launch_tile<true, 128, 128, kOneChunk>(p, st) : launch_tile<true, 128, 128, kAllChunks>(p, st);
+        return one ? launch_tile<false, 64, 128, kOneChunk>(p, st) : launch_tile<false, 64, 128, kAllChunks>(p, st);
+    case kTile128:
+        if (x_is_mx4)
+            return one ? launch_tile<true, 128, 256, kOneChunk>(p, st) : launch_tile<true, 128, 256, kAllChunks>(p, st);
+        return one ? launch_tile<false, 128, 256, kOneChunk>(p, st) : launch_tile<false, 128, 256, kAllChunks>(p, st);
+    case kTile256:
+        return x_is_mx4 ? launch_tile<true, 256, 256, kOneChunk>(p, st) : launch_tile<false, 128, 256, kOneChunk>(p, st);
+    default:
+        break;
     }
     if (x_is_mx4) {
         if (p.M <= 16)

@@ -3,17 +3,21 @@
 // mx4_linear.hip, which states the arithmetic.
 //
 // Steps of 128 k go through a ring of NS stages in LDS, filled by loads that
-// write LDS themselves.  At step j a wave waits until its own loads of stage j
-// have landed, meets the others at the one barrier of the step (then all of
-// stage j is there and stage j - 1 is read out), starts the loads of step
-// j + NS - 1 into the buffer of stage j - 1, and multiplies stage j.
+// write LDS themselves.  A wave reads its operands from LDS a part of a step
+// ahead of their products (half of its rows, MX4 x; one block of 32, bf16 x), so
+// that the matrix cores do not wait for LDS.  Once step j's last operands are in
+// registers it waits until its own loads of stage j + 1 have landed and meets
+// the others at the one barrier of the step: then all of stage j + 1 is there
+// and stage j is read out, so the loads of step j + NS start into its place.
 //
 // LDS layout: 16-byte pieces of a row, in an order that depends on the row, so
 // that the 16 rows a matrix-core operand reads at one k fall on different
 // banks.  The order is applied to the global address each lane loads from
-// (the loads fill LDS in lane order).  Scales: one word (four blocks) of every
-// row a slot, kSlots words deep, read by the byte; a row's scale bytes are
-// contiguous over the chunks, so words are loaded once each, in order.
+// (the loads fill LDS in lane order).  Scales: a row's scale bytes are contiguous
+// over the chunks and are loaded once each, in order, kUnit bytes of every row at
+// a time, into a ring of kScaleRing bytes a row.  kUnit is 16, and a step's four
+// scales are read as one word, where rows are 16-byte aligned and chunks
+// multiples of 128; otherwise it is 4 and they are read by the byte.
 #pragma once
 
 #include "mx4.h"
@@ -21,21 +25,36 @@
 namespace lora {
 
 constexpr int kTileWaves = 8;
-constexpr int kSlots = 8;                    // scale words of a row in flight
+constexpr int kScaleRing = 32;               // scale bytes of a row in LDS: two aligned runs of 16
+
+// What a workgroup does with the chunks of split_k.
+enum TileMode {
+    kOneChunk,                               // there is one
+    kAllChunks,                              // sums them one after another
+    kPartial                                 // computes one and stores its sum to the workspace
+};
 
 typedef __attribute__((address_space(3))) uint8_t lds_u8;
 
-// 64 lanes x 16 (4) bytes from per-lane addresses to LDS at `to` + 16 (4) lane.
-// These write no registers, so the compiler need not know when they land; the
-// kernel waits for them by count (wait_loads).
-__device__ __forceinline__ void load_to_lds16(const uint8_t* from, uint32_t to)
+// Loads of 64 lanes straight to LDS, 16 (4) bytes a lane in lane order.  They
+// write no registers, so the compiler need not know when they land; the kernel
+// waits for them by count (wait_loads_and_meet).
+// From `base` plus a lane's offset to LDS at `to` + AT.
+template <int AT>
+__device__ __forceinline__ void load_to_lds16(const uint8_t* base, uint32_t offset, uint32_t to)
 {
-    asm volatile("s_mov_b32 m0, %1\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %0, off" ::"v"(from), "s"(to) : "memory");
+    asm volatile("s_add_u32 m0, %1, %3\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %0, %2" ::"v"(offset), "s"(to), "s"(base),
+                 "n"(AT)
+                 : "memory", "scc");
 }
 
-__device__ __forceinline__ void load_to_lds4(const uint8_t* from, uint32_t to)
+template <int BYTES>
+__device__ __forceinline__ void load_scales_to_lds(const uint8_t* from, uint32_t to)
 {
-    asm volatile("s_mov_b32 m0, %1\n\ts_nop 0\n\tglobal_load_lds_dword %0, off" ::"v"(from), "s"(to) : "memory");
+    if constexpr (BYTES == 16)
+        asm volatile("s_mov_b32 m0, %1\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %0, off" ::"v"(from), "s"(to) : "memory");
+    else
+        asm volatile("s_mov_b32 m0, %1\n\ts_nop 0\n\tglobal_load_lds_dword %0, off" ::"v"(from), "s"(to) : "memory");
 }
 
 // Waits until at most N of this wave's loads are outstanding and its LDS reads
@@ -46,16 +65,34 @@ __device__ __forceinline__ void wait_loads_and_meet()
     asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)\n\ts_barrier" ::"n"(N) : "memory");
 }
 
-// Where 16-byte piece c of a row goes: rows of 64 bytes (4 pieces) and of 256
-// bytes (16 pieces).
+// What piece number c of a row is combined with to give its place: rows of 64
+// bytes (4 pieces) and of 256 bytes (16 pieces).  A 16-byte read of 64 lanes is
+// served 16 lanes at a time, and these are lanes 0-3, 12-15 and 20-27, then 4-11,
+// 16-19 and 28-31 (and the same of the upper half): with rows in the lanes of a
+// group and pieces in the groups, each 16 then have 16 places mod 256 bytes.
 __device__ __forceinline__ int swizzle4(int row)
 {
-    return ((row >> 1) & 3) ^ ((row >> 3) & 1);
+    return (4 - (row >> 2)) & 3;
 }
 
 __device__ __forceinline__ int swizzle16(int row)
 {
     return row & 15;
+}
+
+template <int N>
+struct Flag {
+    static constexpr int value = N;
+};
+
+// f(Flag<0>()) ... f(Flag<N - 1>())
+template <int N, class F>
+__device__ __forceinline__ void unrolled(F f)
+{
+    if constexpr (N > 0) {
+        unrolled<N - 1>(f);
+        f(Flag<N - 1>());
+    }
 }
 
 template <bool XMX, int TM, int TN>
@@ -68,14 +105,15 @@ struct TileShape {
     static constexpr int kWLoads = kWStage / (kTileWaves * 1024);
     static constexpr int kScaleRows = TN + (XMX ? TM : 0);   // W's rows first
     static constexpr int kScaleWaves = kScaleRows / 64;
+    static_assert(kScaleWaves <= kTileWaves, "a wave loads the scales of at most 64 rows");
     static constexpr int kRows = TM / 32, kCols = TN / 64;   // 16 x 16 tiles of a wave
-    static constexpr int kBudget = 160 * 1024 - kSlots * kScaleRows * 4;
+    static constexpr int kBudget = 160 * 1024 - kScaleRing * kScaleRows;
     static constexpr int kStages = kBudget / kStage < 4 ? kBudget / kStage : 4;
-    static constexpr int kLds = kStages * kStage + kSlots * kScaleRows * 4;
+    static constexpr int kLds = kStages * kStage + kScaleRing * kScaleRows;
     static_assert(kXLoads >= 1 && kWLoads >= 1 && kStages >= 2, "tile too small or too large");
 };
 
-template <bool XMX, int TM, int TN, bool SPLIT>
+template <bool XMX, int TM, int TN, TileMode MODE, int kUnit>
 __global__ void __launch_bounds__(kTileWaves * 64, 2) k_mx4_linear_tile(Mx4LinearParams p)
 {
     using T = TileShape<XMX, TM, TN>;
@@ -101,32 +139,32 @@ __global__ void __launch_bounds__(kTileWaves * 64, 2) k_mx4_linear_tile(Mx4Linea
     const int64_t m0 = (int64_t)(strip * kStrip + in_strip % strip_rows) * TM;
     const int64_t n0 = (int64_t)(in_strip / strip_rows) * TN;
 
-    // per-lane sources: a piece's place in LDS is its load's place in the
-    // stage, load i of wave w filling 1024 bytes from (i * 8 + w) * 1024
-    const uint8_t* xsrc[T::kXLoads];
-    int xblock[T::kXLoads];
+    // Sources: load i of wave w fills 1024 bytes of a stage from (i * 8 + w) * 1024,
+    // x's rows, then W's.  A lane's offset from its tile's first row, and the one
+    // of a chunk's ragged last step, where blocks past the chunk's end load the
+    // step's first block instead.
+    const int rem = p.k_chunk % 128 / kMxBlock;                // blocks of that step, 0: there is none
+    uint32_t xoff[2][T::kXLoads], woff[2][T::kWLoads];
 #pragma unroll
     for (int i = 0; i < T::kXLoads; ++i) {
         constexpr int P = T::kXBytes / 16;
         const int piece = (i * kTileWaves + wave) * 64 + lane;
         const int row = piece / P;
         const int c = (piece % P) ^ (XMX ? swizzle4(row) : swizzle16(row));
-        const int64_t m = min(m0 + row, p.M - 1);
-        xblock[i] = XMX ? c : c >> 2;
-        xsrc[i] = static_cast<const uint8_t*>(p.x) + m * p.ld_x * (XMX ? 1 : 2) + c * 16;
+        const uint32_t m = (uint32_t)(min(m0 + row, p.M - 1) - m0);
+        xoff[0][i] = m * (uint32_t)(p.ld_x * (XMX ? 1 : 2)) + c * 16;
+        xoff[1][i] = xoff[0][i] - ((XMX ? c : c >> 2) < rem ? 0 : XMX ? c * 16 : c / 4 * 64);
     }
-    const uint8_t* wsrc[T::kWLoads];
-    int wblock[T::kWLoads];
 #pragma unroll
     for (int i = 0; i < T::kWLoads; ++i) {
         const int piece = (i * kTileWaves + wave) * 64 + lane;
         const int row = piece / 4;
         const int c = (piece % 4) ^ swizzle4(row);
-        const int64_t n = min(n0 + row, p.N - 1);
-        wblock[i] = c;
-        wsrc[i] = p.wq + n * p.ld_wq + c * 16;
+        const uint32_t n = (uint32_t)(min(n0 + row, p.N - 1) - n0);
+        woff[0][i] = n * (uint32_t)p.ld_wq + c * 16;
+        woff[1][i] = woff[0][i] - (c < rem ? 0 : c * 16);
     }
-    const uint8_t* ssrc = nullptr;
+    const uint8_t* ssrc = p.ws;              // this lane's row of scales
     {
         const int row = wave * 64 + lane;
         if (row < TN)
@@ -135,44 +173,49 @@ __global__ void __launch_bounds__(kTileWaves * 64, 2) k_mx4_linear_tile(Mx4Linea
             ssrc = p.xs + min(m0 + row - TN, p.M - 1) * p.ld_xs;
     }
 
-    const int chunk_steps = (p.k_chunk + 127) / 128;
-    const int steps = chunk_steps * p.split_k;
-    const int last_word = (p.k_chunk / kMxBlock * p.split_k - 1) >> 2;
-    int words = 0;                           // scale words whose loads have been started
+    const int chunk_steps = (p.k_chunk + 127) / 128, whole_steps = p.k_chunk / 128;
+    const int chunks = MODE == kAllChunks ? p.split_k : 1;
+    const int steps = chunk_steps * chunks;
+    const uint32_t b_first = MODE == kPartial ? blockIdx.y * (uint32_t)(p.k_chunk / kMxBlock) : 0;
+    const uint32_t last_unit = ((uint32_t)(p.k_chunk / kMxBlock * p.split_k) - 1) / kUnit;
 
-    // the step whose loads come next: its number within the chunk and its k
-    int next_t = 0;
-    int64_t next_k = 0;
-    int next_stage = 0;
-    auto start_loads = [&]() {
-        const uint32_t base = lds0 + next_stage * T::kStage;
-        const int left = p.k_chunk - next_t * 128;           // k left in the chunk
-#pragma unroll
-        for (int i = 0; i < T::kXLoads; ++i) {
-            // blocks past the chunk's end load the step's first block instead
-            const int64_t back = xblock[i] * kMxBlock < left ? 0 : xblock[i] * (XMX ? 16 : 64);
-            load_to_lds16(xsrc[i] + (XMX ? next_k / 2 : next_k * 2) - back,
-                          __builtin_amdgcn_readfirstlane(base + (i * kTileWaves + wave) * 1024));
-        }
-#pragma unroll
-        for (int i = 0; i < T::kWLoads; ++i) {
-            const int64_t back = wblock[i] * kMxBlock < left ? 0 : wblock[i] * 16;
-            load_to_lds16(wsrc[i] + next_k / 2 - back,
-                          __builtin_amdgcn_readfirstlane(base + T::kXStage + (i * kTileWaves + wave) * 1024));
-        }
-        const int need = min((int)((next_k / kMxBlock + 3) >> 2), last_word);
-        if (words <= need) {                 // at most one more word a step
-            if (wave < T::kScaleWaves)
-                load_to_lds4(ssrc + words * 4,
-                             __builtin_amdgcn_readfirstlane(lds0 + T::kStages * T::kStage +
-                                                            ((words % kSlots) * T::kScaleRows + wave * 64) * 4));
-            ++words;
-        }
-        next_k += min(left, 128);
-        next_t = next_t + 1 == chunk_steps ? 0 : next_t + 1;
-        next_stage = next_stage + 1 == T::kStages ? 0 : next_stage + 1;
+    uint32_t units = b_first / kUnit;        // scale units whose loads have been started
+    auto load_unit = [&]() {
+        if (wave < T::kScaleWaves)
+            load_scales_to_lds<kUnit>(ssrc + (uint64_t)units * kUnit,
+                                      lds0 + T::kStages * T::kStage +
+                                          (units % (kScaleRing / kUnit) * T::kScaleRows + wave * 64) * kUnit);
+        ++units;
     };
+    // loads of one step into the stage at `slot`; ld_* is the step whose loads
+    // come next
+    uint32_t slot = 0, ld_block = b_first;
+    int ld_t = 0;
+    const uint8_t* xbase = static_cast<const uint8_t*>(p.x) + m0 * p.ld_x * (XMX ? 1 : 2) +
+                           (uint64_t)b_first * (XMX ? 16 : 64);
+    const uint8_t* wbase = p.wq + n0 * p.ld_wq + (uint64_t)b_first * 16;
+    auto start_loads = [&]() {
+        const uint32_t to = lds0 + slot + wave * 1024;
+        const bool ragged = ld_t == whole_steps;
+        unrolled<T::kXLoads>([&](auto i) {
+            load_to_lds16<i.value * kTileWaves * 1024>(xbase, ragged ? xoff[1][i.value] : xoff[0][i.value], to);
+        });
+        unrolled<T::kWLoads>([&](auto i) {
+            load_to_lds16<T::kXStage + i.value * kTileWaves * 1024>(
+                wbase, ragged ? woff[1][i.value] : woff[0][i.value], to);
+        });
+        // a step's four scale bytes end at most one unit past the step before's
+        if (units <= min((ld_block + 3) / kUnit, last_unit))
+            load_unit();
+        const int blocks = ragged ? rem : 4;
+        ld_block += blocks;
+        xbase += blocks * (XMX ? 16 : 64);
+        wbase += blocks * 16;
+        ld_t = ld_t + 1 == chunk_steps ? 0 : ld_t + 1;
+    };
+    auto next_slot = [&]() { slot = slot + T::kStage == T::kStages * T::kStage ? 0 : slot + T::kStage; };
 
+    constexpr bool SPLIT = MODE == kAllChunks;
     f32x4 acc[T::kRows][T::kCols], tot[SPLIT ? T::kRows : 1][T::kCols];
 #pragma unroll
     for (int r = 0; r < T::kRows; ++r)
@@ -180,95 +223,203 @@ __global__ void __launch_bounds__(kTileWaves * 64, 2) k_mx4_linear_tile(Mx4Linea
         for (int c = 0; c < T::kCols; ++c)
             acc[r][c] = f32x4{0, 0, 0, 0};
 
-    for (int j = 0; j < T::kStages - 1; ++j)
+    // a chunk that starts inside a unit may need two for its first step
+    if (MODE == kPartial && units < last_unit)
+        load_unit();
+    for (int j = 0; j < T::kStages; ++j) {
         if (j < steps)
             start_loads();
+        next_slot();
+    }
+    int ld_left = steps - T::kStages;
+    // Of the loads in flight, those of later steps may stay so.  Scale units, which
+    // not every step has, are not counted among them.
+    constexpr int kStepLoads = T::kXLoads + T::kWLoads;
+    if (T::kStages <= steps)
+        wait_loads_and_meet<(T::kStages - 1) * kStepLoads>();
+    else
+        wait_loads_and_meet<0>();
 
-    int t = 0, chunk = 0, stage = 0;
-    int64_t k = 0;
-    for (int j = 0; j < steps; ++j) {
-        // the loads of the steps after j may still be on their way
-        constexpr int kStepLoads = T::kXLoads + T::kWLoads;
-        if (j + T::kStages - 2 < steps)
-            wait_loads_and_meet<(T::kStages - 2) * kStepLoads>();
-        else
-            wait_loads_and_meet<0>();
-        if (j + T::kStages - 1 < steps)
+    // On to the next step, once stage j + 1 has landed everywhere and stage j is
+    // read out: its place takes the loads of step j + NS.  What is read from here on
+    // is stage j + 1, at `slot`, whose first block is rd_block.
+    uint32_t rd_block = b_first;
+    auto next_step = [&](auto tail, auto drain) {
+        wait_loads_and_meet<decltype(drain)::value ? 0 : (T::kStages - 2) * kStepLoads>();
+        if (ld_left-- > 0)
             start_loads();
+        next_slot();
+        rd_block += decltype(tail)::value ? rem : 4;
+    };
+    // the scale of one block, of row 0 (rows are kUnit bytes apart)
+    auto scale_bytes = [&](uint32_t block) {
+        return lds + T::kStages * T::kStage + block / kUnit % (kScaleRing / kUnit) * (T::kScaleRows * kUnit) +
+               block % kUnit;
+    };
+    const int wrow = wn * (TN / 4) + li, xrow = wm * (TM / 2) + li;
+    // rows 16 apart have the same order of pieces
+    const uint32_t wat = T::kXStage + wrow * 64, wsw = swizzle4(wrow);
+    const uint32_t xat = xrow * T::kXBytes, xsw = XMX ? swizzle4(xrow) : swizzle16(xrow);
 
-        const uint8_t* xs = lds + stage * T::kStage;
-        const uint8_t* ws = xs + T::kXStage;
-        const int left = p.k_chunk - t * 128;
-        // the scale of one block, of row 0 (rows are 4 bytes apart)
-        auto scale_bytes = [&](int block) {
-            return lds + T::kStages * T::kStage + ((block >> 2) % kSlots) * (T::kScaleRows * 4) + (block & 3);
-        };
+    // what a wave has in registers between steps
+    constexpr int kHalf = T::kRows / 2;
+    MxOperand w[T::kCols], xa[kHalf], xb[kHalf];               // MX4 x
+    u32x4 wq[T::kCols], even[T::kRows], odd[T::kRows];         // bf16 x
+    uint32_t ws4[T::kCols];
 
-        if constexpr (XMX) {
-            const bool ok = g * kMxBlock < left;
-            const int block = (int)(k / kMxBlock) + g;
-            const uint8_t* sc = scale_bytes(block);
-            MxOperand w[T::kCols];
+    auto read_w = [&](int c) {
+        w[c].q = *reinterpret_cast<const u32x4*>(lds + slot + wat + (g ^ wsw) * 16 + c * 1024);
+        w[c].s = scale_bytes(rd_block + g)[(wrow + 16 * c) * kUnit];
+    };
+    auto read_x = [&](MxOperand (&x)[kHalf], int first) {
 #pragma unroll
-            for (int c = 0; c < T::kCols; ++c) {
-                const int row = wn * (TN / 4) + 16 * c + li;
-                w[c].q = *reinterpret_cast<const u32x4*>(ws + row * 64 + ((g ^ swizzle4(row)) * 16));
-                w[c].s = sc[row * 4];
-                if (!ok)
-                    w[c] = MxOperand{u32x4{0, 0, 0, 0}, 127};
-            }
+        for (int r = 0; r < kHalf; ++r) {
+            x[r].q = *reinterpret_cast<const u32x4*>(lds + slot + xat + (g ^ xsw) * 16 +
+                                                     (first + r) * 1024);
+            x[r].s = scale_bytes(rd_block + g)[(TN + xrow + 16 * (first + r)) * kUnit];
+        }
+    };
+    // bf16 x: W's codes of a step, block g in lane group g, and its scales
+    auto read_codes = [&](u32x4 (&q)[T::kCols], uint32_t (&s)[T::kCols]) {
 #pragma unroll
-            for (int r = 0; r < T::kRows; ++r) {
-                const int row = wm * (TM / 2) + 16 * r + li;
-                MxOperand x;
-                x.q = *reinterpret_cast<const u32x4*>(xs + row * 64 + ((g ^ swizzle4(row)) * 16));
-                x.s = sc[(TN + row) * 4];
-                if (!ok)
-                    x = MxOperand{u32x4{0, 0, 0, 0}, 127};
+        for (int c = 0; c < T::kCols; ++c) {
+            q[c] = *reinterpret_cast<const u32x4*>(lds + slot + wat + (g ^ wsw) * 16 + c * 1024);
+            const int row = (wrow + 16 * c) * kUnit;
+            if constexpr (kUnit == 16) {
+                s[c] = *reinterpret_cast<const uint32_t*>(scale_bytes(rd_block) + row);
+            } else {
+                s[c] = 0;
 #pragma unroll
-                for (int c = 0; c < T::kCols; ++c)
-                    acc[r][c] = mfma_mx4(w[c], x, acc[r][c]);
-            }
-        } else {
-#pragma unroll
-            for (int s = 0; s < 4; ++s) {
-                if (s * kMxBlock >= left)
-                    break;
-                const uint8_t* sc = scale_bytes((int)(k / kMxBlock) + s);
-                bf16x8 wb[T::kCols];
-#pragma unroll
-                for (int c = 0; c < T::kCols; ++c) {
-                    const int row = wn * (TN / 4) + 16 * c + li;
-                    const uint32_t q = *reinterpret_cast<const uint32_t*>(ws + row * 64 + ((s ^ swizzle4(row)) * 16) + 4 * g);
-                    wb[c] = mx4_to_bf16(q, mx_scale_f32(sc[row * 4]));
-                }
-#pragma unroll
-                for (int r = 0; r < T::kRows; ++r) {
-                    const int row = wm * (TM / 2) + 16 * r + li;
-                    const u32x4 x = *reinterpret_cast<const u32x4*>(xs + row * 256 + (((4 * s + g) ^ swizzle16(row)) * 16));
-#pragma unroll
-                    for (int c = 0; c < T::kCols; ++c)
-                        acc[r][c] = mfma_16x16x32(wb[c], __builtin_bit_cast(bf16x8, x), acc[r][c]);
-                }
+                for (int e = 0; e < 4; ++e)
+                    s[c] |= (uint32_t)scale_bytes(rd_block + e)[row] << (8 * e);
             }
         }
-
-        k += min(left, 128);
-        stage = stage + 1 == T::kStages ? 0 : stage + 1;
-        if (++t == chunk_steps) {
-            t = 0;
-            if constexpr (SPLIT) {
+    };
+    auto read_block = [&](u32x4 (&x)[T::kRows], uint32_t s) {
 #pragma unroll
-                for (int r = 0; r < T::kRows; ++r)
+        for (int r = 0; r < T::kRows; ++r)
+            x[r] = *reinterpret_cast<const u32x4*>(lds + slot + xat + ((4 * s + g) ^ xsw) * 16 +
+                                                   r * 4096);
+    };
+    // blocks past the chunk's end enter as zeros
+    auto clear = [&](auto& o) {
+        for (auto& v : o)
+            if (g >= rem)
+                v = MxOperand{u32x4{0, 0, 0, 0}, 127};
+    };
+    auto products = [&](u32x4 (&x)[T::kRows], int s) {
+        bf16x8 wb[T::kCols];
 #pragma unroll
-                    for (int c = 0; c < T::kCols; ++c) {
+        for (int c = 0; c < T::kCols; ++c)
+            wb[c] = mx4_to_bf16(wq[c][s], mx_scale_f32((ws4[c] >> (8 * s)) & 255u));
 #pragma unroll
-                        for (int e = 0; e < 4; ++e)
-                            tot[r][c][e] = chunk == 0 ? acc[r][c][e] : tot[r][c][e] + acc[r][c][e];
-                        acc[r][c] = f32x4{0, 0, 0, 0};
-                    }
-                ++chunk;
+        for (int r = 0; r < T::kRows; ++r)
+#pragma unroll
+            for (int c = 0; c < T::kCols; ++c)
+                acc[r][c] = mfma_16x16x32(wb[c], __builtin_bit_cast(bf16x8, x[r]), acc[r][c]);
+    };
+    auto take_codes = [&](u32x4 (&q)[T::kCols], uint32_t (&s)[T::kCols]) {
+#pragma unroll
+        for (int c = 0; c < T::kCols; ++c) {
+            wq[c] = q[c];
+            ws4[c] = s[c];
+            transpose_groups(wq[c]);
+        }
+    };
+    // One step.  It has no branches (but for a chunk's ragged last step), so that
+    // the order of reads and products written here is the order they run in.
+    // drain: the stages in flight are no longer NS.
+    auto step = [&](auto tail, auto drain) {
+        constexpr bool TAIL = decltype(tail)::value != 0;
+        if constexpr (XMX) {
+            read_x(xb, kHalf);
+            __builtin_amdgcn_sched_barrier(0);
+            if constexpr (TAIL) {
+                clear(w);
+                clear(xa);
             }
+#pragma unroll
+            for (int c = 0; c < T::kCols; ++c)
+#pragma unroll
+                for (int r = 0; r < kHalf; ++r)
+                    acc[r][c] = mfma_mx4(w[c], xa[r], acc[r][c]);
+            __builtin_amdgcn_sched_barrier(0);
+            next_step(tail, drain);
+            read_x(xa, 0);
+            __builtin_amdgcn_sched_barrier(0);
+            if constexpr (TAIL)
+                clear(xb);
+            // a column's W is read for the next step as soon as its last product
+            // has started
+#pragma unroll
+            for (int c = 0; c < T::kCols; ++c) {
+#pragma unroll
+                for (int r = 0; r < kHalf; ++r)
+                    acc[kHalf + r][c] = mfma_mx4(w[c], xb[r], acc[kHalf + r][c]);
+                __builtin_amdgcn_sched_barrier(0);
+                read_w(c);
+                __builtin_amdgcn_sched_barrier(0);
+            }
+        } else {
+            read_block(odd, 1);
+            __builtin_amdgcn_sched_barrier(0);
+            products(even, 0);
+            __builtin_amdgcn_sched_barrier(0);
+            read_block(even, 2);
+            __builtin_amdgcn_sched_barrier(0);
+            if (!TAIL || rem > 1)
+                products(odd, 1);
+            __builtin_amdgcn_sched_barrier(0);
+            read_block(odd, 3);
+            __builtin_amdgcn_sched_barrier(0);
+            if (!TAIL || rem > 2)
+                products(even, 2);
+            __builtin_amdgcn_sched_barrier(0);
+            next_step(tail, drain);
+            u32x4 q[T::kCols];
+            uint32_t s4[T::kCols];
+            read_codes(q, s4);
+            read_block(even, 0);
+            __builtin_amdgcn_sched_barrier(0);
+            if constexpr (!TAIL)
+                products(odd, 3);
+            __builtin_amdgcn_sched_barrier(0);
+            take_codes(q, s4);
+        }
+    };
+
+    if constexpr (XMX) {
+#pragma unroll
+        for (int c = 0; c < T::kCols; ++c)
+            read_w(c);
+        read_x(xa, 0);
+    } else {
+        u32x4 q[T::kCols];
+        uint32_t s4[T::kCols];
+        read_codes(q, s4);
+        take_codes(q, s4);
+        read_block(even, 0);
+    }
+    int full = steps - T::kStages + 1;       // steps with all the later stages in flight
+    for (int chunk = 0; chunk < chunks; ++chunk) {
+        const int n = max(0, min(full, whole_steps));
+        for (int t = 0; t < n; ++t)
+            step(Flag<0>(), Flag<0>());
+        for (int t = n; t < whole_steps; ++t)
+            step(Flag<0>(), Flag<1>());
+        if (rem)
+            step(Flag<1>(), Flag<1>());
+        full -= chunk_steps;
+        if constexpr (SPLIT) {
+#pragma unroll
+            for (int r = 0; r < T::kRows; ++r)
+#pragma unroll
+                for (int c = 0; c < T::kCols; ++c) {
+#pragma unroll
+                    for (int e = 0; e < 4; ++e)
+                        tot[r][c][e] = chunk == 0 ? acc[r][c][e] : tot[r][c][e] + acc[r][c][e];
+                    acc[r][c] = f32x4{0, 0, 0, 0};
+                }
         }
     }
 
@@ -279,7 +430,11 @@ __global__ void __launch_bounds__(kTileWaves * 64, 2) k_mx4_linear_tile(Mx4Linea
         for (int c = 0; c < T::kCols; ++c) {
             const int64_t n = n0 + wn * (TN / 4) + 16 * c + 4 * g;
             const f32x4 v = SPLIT ? tot[SPLIT ? r : 0][c] : acc[r][c];
-            if (m < p.M && n < p.N) {
+            if (m >= p.M || n >= p.N)
+                continue;
+            if constexpr (MODE == kPartial) {
+                *reinterpret_cast<f32x4*>(p.partial + ((int64_t)blockIdx.y * p.M + m) * p.N + n) = v;
+            } else {
                 const uint32_t lo = f32_to_bf16_bits(v[0]) | (uint32_t)f32_to_bf16_bits(v[1]) << 16;
                 const uint32_t hi = f32_to_bf16_bits(v[2]) | (uint32_t)f32_to_bf16_bits(v[3]) << 16;
                 *reinterpret_cast<u32x2*>(p.y + m * p.ld_y + n) = u32x2{lo, hi};
@@ -288,12 +443,17 @@ __global__ void __launch_bounds__(kTileWaves * 64, 2) k_mx4_linear_tile(Mx4Linea
     }
 }
 
-template <bool XMX, int TM, int TN, bool SPLIT>
+template <bool XMX, int TM, int TN, TileMode MODE>
 hipError_t launch_tile(const Mx4LinearParams& p, hipStream_t st)
 {
     const int64_t tiles = ((p.M + TM - 1) / TM) * ((p.N + TN - 1) / TN);
-    hipLaunchKernelGGL((k_mx4_linear_tile<XMX, TM, TN, SPLIT>), dim3((unsigned)tiles), dim3(kTileWaves * 64), 0, st,
-                       p);
+    const dim3 grid((unsigned)tiles, MODE == kPartial ? (unsigned)p.split_k : 1u), block(kTileWaves * 64);
+    const uintptr_t rows = reinterpret_cast<uintptr_t>(p.ws) | (uintptr_t)p.ld_ws |
+                           (XMX ? reinterpret_cast<uintptr_t>(p.xs) | (uintptr_t)p.ld_xs : 0);
+    if (rows % 16 == 0 && (p.split_k == 1 || p.k_chunk % 128 == 0))
+        hipLaunchKernelGGL((k_mx4_linear_tile<XMX, TM, TN, MODE, 16>), grid, block, 0, st, p);
+    else
+        hipLaunchKernelGGL((k_mx4_linear_tile<XMX, TM, TN, MODE, 4>), grid, block, 0, st, p);
     return hipGetLastError();
 }
 

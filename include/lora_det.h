@@ -513,7 +513,7 @@ int lora_sgmv_expand(const float* h, int64_t ld_h, const uint16_t* const* B_ptrs
  *           4-byte aligned, ld_s % 4 == 0, ld_s >= K / 32 (so every row's last
  *           aligned word can be read; bytes past K / 32 are ignored and left
  *           as they are)
- * Leading dimensions of MX4 operands, and of a product's x, are at most 2^25
+ * Leading dimensions of MX4 operands, and of a product's x, are at most 2^23
  * bytes.
  * ------------------------------------------------------------------------- */
 
