@@ -13,7 +13,6 @@
 // The "row" operand is W, so a lane's accumulator holds four consecutive output
 // columns of one token.
 #include "mx4_tile.h"
-#include <stdlib.h>
 
 namespace lora {
 
@@ -302,46 +301,88 @@ hipError_t launch_split_tile(const Mx4LinearParams& p, hipStream_t st)
     return hipGetLastError();
 }
 
-// Which kernel a call takes.
-enum Schedule { kRows, kSplit64, kTile64, kTile128, kTile256 };
+// Which kernel a call takes: the one of least estimated time.  The estimates, in
+// ns, come from measurements on MI355X (K, N of 4096 .. 28672, M of 1 .. 4096, every
+// split_k) and are within about 15% of them:
+//   rows    a chain's steps of 128 k follow one another, and a CU shares its waves'
+//           loads: by tiles of 16 tokens, one step alone / per CU
+//   tiles   a workgroup a CU, steps of 128 k one after another
+//   split   the smallest tiles, a chunk a workgroup, then the joining launch, which
+//           moves 8 bytes an output and chunk
+// e.g. bf16 x, 200 x 4096 x 6144, split_k 4: 64 x 128 tiles 24.7 us, split 31, rows
+// 85, 128 x 256 tiles 56; 33 x 14336 x 4096, split_k 8: split 17.7, rows 36.5.
+enum Schedule { kRows, kSplit, kTileSmall, kTileMiddle, kTileLarge };
 
-Schedule schedule_for(int64_t M, int64_t N, int32_t k_chunk, int32_t split_k, bool x_is_mx4)
+constexpr int64_t kCus = 256;
+
+int64_t ceil_div(int64_t a, int64_t b)
 {
-    if (const char* e = getenv("MX4_SCHED")) return (Schedule)atoi(e);  // EXPERIMENT
-    if (M <= 64)
-        return kRows;
-    return split_k > 1 || !x_is_mx4 ? kTile128 : kTile256;
+    return (a + b - 1) / b;
+}
+
+Schedule schedule_for(int64_t M, int64_t N, int32_t k_chunk, int32_t split_k, bool mx)
+{
+    const int64_t chunk_steps = ceil_div(k_chunk, kStepK), steps = chunk_steps * split_k;
+    // rows: blocks of up to 64 tokens
+    const int64_t alone[2][4] = {{600, 1050, 1600, 2250}, {300, 430, 680, 680}};
+    const int64_t shared[2][4] = {{180, 300, 400, 540}, {100, 125, 190, 190}};
+    const int64_t tiles = M < 64 ? ceil_div(M, 16) : 4;
+    const int64_t waves = ceil_div(M, 64) * ceil_div(N, 16) * split_k;
+    const int64_t one = chunk_steps * alone[mx][tiles - 1];
+    const int64_t all = ceil_div(waves, kCus) * chunk_steps * shared[mx][tiles - 1];
+    Schedule best = kRows;
+    int64_t least = 2000 + (one > all ? one : all);
+    auto consider = [&](Schedule s, int64_t ns) {
+        if (ns < least) {
+            least = ns;
+            best = s;
+        }
+    };
+    auto rounds = [&](int64_t tm, int64_t tn, int64_t copies) {
+        return ceil_div(ceil_div(M, tm) * ceil_div(N, tn) * copies, kCus);
+    };
+    const int64_t tm = mx ? 128 : 64, small = mx ? 520 : 740;
+    consider(kTileSmall, 2000 + rounds(tm, 128, 1) * steps * small);
+    consider(kTileMiddle, 2000 + rounds(128, 256, 1) * steps * (mx ? 720 : split_k > 1 ? 1700 : 1530));
+    if (mx && split_k == 1)
+        consider(kTileLarge, 2000 + rounds(256, 256, 1) * steps * 1100);
+    if (split_k > 1)
+        consider(kSplit, 6500 + rounds(tm, 128, split_k) * chunk_steps * small + M * N * split_k * 8 / 4000);
+    return best;
 }
 
 }  // namespace
 
 int64_t mx4_linear_workspace(int64_t M, int64_t N, int32_t k_chunk, int32_t split_k, bool x_is_mx4)
 {
-    return schedule_for(M, N, k_chunk, split_k, x_is_mx4) == kSplit64 ? M * N * split_k * (int64_t)sizeof(float) : 0;
+    return schedule_for(M, N, k_chunk, split_k, x_is_mx4) == kSplit ? M * N * split_k * (int64_t)sizeof(float) : 0;
 }
 
 hipError_t launch_mx4_linear(const Mx4LinearParams& p, bool x_is_mx4, hipStream_t st)
 {
     const bool one = p.split_k == 1;
     switch (schedule_for(p.M, p.N, p.k_chunk, p.split_k, x_is_mx4)) {
-    case kSplit64:
+    case kSplit:
         return x_is_mx4 ? launch_split_tile<true, 128, 128>(p, st) : launch_split_tile<false, 64, 128>(p, st);
-    case kTile64:
+    case kTileSmall:
         if (x_is_mx4)
             return one ? launch_tile<true, 128, 128, kOneChunk>(p, st) : launch_tile<true, 128, 128, kAllChunks>(p, st);
         return one ? launch_tile<false, 64, 128, kOneChunk>(p, st) : launch_tile<false, 64, 128, kAllChunks>(p, st);
-    case kTile128:
+    case kTileMiddle:
         if (x_is_mx4)
             return one ? launch_tile<true, 128, 256, kOneChunk>(p, st) : launch_tile<true, 128, 256, kAllChunks>(p, st);
         return one ? launch_tile<false, 128, 256, kOneChunk>(p, st) : launch_tile<false, 128, 256, kAllChunks>(p, st);
-    case kTile256:
-        return x_is_mx4 ? launch_tile<true, 256, 256, kOneChunk>(p, st) : launch_tile<false, 128, 256, kOneChunk>(p, st);
+    case kTileLarge:
+        return launch_tile<true, 256, 256, kOneChunk>(p, st);
     default:
         break;
     }
     if (x_is_mx4) {
+        // eight steps ahead where a chain has more than four: 16 x 8192 x 8192 in 8
+        // chunks 11.9 us against 15.1; in 16 chunks of four steps 13.7 against 19.4
         if (p.M <= 16)
-            return launch_rows<true, 1, 1, 8, 4, 1024>(p, st);
+            return p.k_chunk > 4 * kStepK ? launch_rows<true, 1, 1, 8, 4, 1024>(p, st)
+                                          : launch_rows<true, 1, 1, 4, 4, 1024>(p, st);
         if (p.M <= 32)
             return launch_rows<true, 2, 1, 4, 2, 1024>(p, st);
         return launch_rows<true, 4, 1, 2, 2, 1024>(p, st);

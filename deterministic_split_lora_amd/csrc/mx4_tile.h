@@ -194,20 +194,23 @@ __global__ void __launch_bounds__(kTileWaves * 64, 2) k_mx4_linear_tile(Mx4Linea
     const uint8_t* xbase = static_cast<const uint8_t*>(p.x) + m0 * p.ld_x * (XMX ? 1 : 2) +
                            (uint64_t)b_first * (XMX ? 16 : 64);
     const uint8_t* wbase = p.wq + n0 * p.ld_wq + (uint64_t)b_first * 16;
-    auto start_loads = [&]() {
-        const uint32_t to = lds0 + slot + wave * 1024;
+    constexpr int kStepLoads = T::kXLoads + T::kWLoads;
+    // load i of kStepLoads of the step, into the stage at `at`
+    auto load_piece = [&](auto i, uint32_t at) {
+        constexpr int I = decltype(i)::value;
+        const uint32_t to = lds0 + at + wave * 1024;
         const bool ragged = ld_t == whole_steps;
-        unrolled<T::kXLoads>([&](auto i) {
-            load_to_lds16<i.value * kTileWaves * 1024>(xbase, ragged ? xoff[1][i.value] : xoff[0][i.value], to);
-        });
-        unrolled<T::kWLoads>([&](auto i) {
-            load_to_lds16<T::kXStage + i.value * kTileWaves * 1024>(
-                wbase, ragged ? woff[1][i.value] : woff[0][i.value], to);
-        });
+        if constexpr (I < T::kXLoads)
+            load_to_lds16<I * kTileWaves * 1024>(xbase, ragged ? xoff[1][I] : xoff[0][I], to);
+        else
+            load_to_lds16<I * kTileWaves * 1024>(wbase, ragged ? woff[1][I - T::kXLoads] : woff[0][I - T::kXLoads], to);
+    };
+    // after the last of them
+    auto end_loads = [&]() {
         // a step's four scale bytes end at most one unit past the step before's
         if (units <= min((ld_block + 3) / kUnit, last_unit))
             load_unit();
-        const int blocks = ragged ? rem : 4;
+        const int blocks = ld_t == whole_steps ? rem : 4;
         ld_block += blocks;
         xbase += blocks * (XMX ? 16 : 64);
         wbase += blocks * 16;
@@ -227,29 +230,29 @@ __global__ void __launch_bounds__(kTileWaves * 64, 2) k_mx4_linear_tile(Mx4Linea
     if (MODE == kPartial && units < last_unit)
         load_unit();
     for (int j = 0; j < T::kStages; ++j) {
-        if (j < steps)
-            start_loads();
+        if (j < steps) {
+            unrolled<kStepLoads>([&](auto i) { load_piece(i, slot); });
+            end_loads();
+        }
         next_slot();
     }
-    int ld_left = steps - T::kStages;
     // Of the loads in flight, those of later steps may stay so.  Scale units, which
     // not every step has, are not counted among them.
-    constexpr int kStepLoads = T::kXLoads + T::kWLoads;
     if (T::kStages <= steps)
         wait_loads_and_meet<(T::kStages - 1) * kStepLoads>();
     else
         wait_loads_and_meet<0>();
 
     // On to the next step, once stage j + 1 has landed everywhere and stage j is
-    // read out: its place takes the loads of step j + NS.  What is read from here on
-    // is stage j + 1, at `slot`, whose first block is rd_block.
+    // read out: its place, the value, takes the loads of step j + NS.  What is read
+    // from here on is stage j + 1, at `slot`, whose first block is rd_block.
     uint32_t rd_block = b_first;
     auto next_step = [&](auto tail, auto drain) {
         wait_loads_and_meet<decltype(drain)::value ? 0 : (T::kStages - 2) * kStepLoads>();
-        if (ld_left-- > 0)
-            start_loads();
+        const uint32_t freed = slot;
         next_slot();
         rd_block += decltype(tail)::value ? rem : 4;
+        return freed;
     };
     // the scale of one block, of row 0 (rows are kUnit bytes apart)
     auto scale_bytes = [&](uint32_t block) {
@@ -266,6 +269,7 @@ __global__ void __launch_bounds__(kTileWaves * 64, 2) k_mx4_linear_tile(Mx4Linea
     MxOperand w[T::kCols], xa[kHalf], xb[kHalf];               // MX4 x
     u32x4 wq[T::kCols], even[T::kRows], odd[T::kRows];         // bf16 x
     uint32_t ws4[T::kCols];
+    bf16x8 wb[2][T::kCols];
 
     auto read_w = [&](int c) {
         w[c].q = *reinterpret_cast<const u32x4*>(lds + slot + wat + (g ^ wsw) * 16 + c * 1024);
@@ -307,16 +311,35 @@ __global__ void __launch_bounds__(kTileWaves * 64, 2) k_mx4_linear_tile(Mx4Linea
             if (g >= rem)
                 v = MxOperand{u32x4{0, 0, 0, 0}, 127};
     };
-    auto products = [&](u32x4 (&x)[T::kRows], int s) {
-        bf16x8 wb[T::kCols];
+    auto convert = [&](bf16x8 (&to)[T::kCols], int s) {
 #pragma unroll
         for (int c = 0; c < T::kCols; ++c)
-            wb[c] = mx4_to_bf16(wq[c][s], mx_scale_f32((ws4[c] >> (8 * s)) & 255u));
+            to[c] = mx4_to_bf16(wq[c][s], mx_scale_f32((ws4[c] >> (8 * s)) & 255u));
+    };
+    auto row_products = [&](bf16x8 (&wv)[T::kCols], u32x4 (&x)[T::kRows], int r) {
+#pragma unroll
+        for (int c = 0; c < T::kCols; ++c)
+            acc[r][c] = mfma_16x16x32(wv[c], __builtin_bit_cast(bf16x8, x[r]), acc[r][c]);
+    };
+    // the products of block s and, between them (the vector unit is free while a
+    // matrix instruction runs), the conversion of block s + 1's W, if there are
+    // registers for both
+    constexpr bool kBetween = !SPLIT || T::kRows <= 2;
+    auto products = [&](u32x4 (&x)[T::kRows], auto s) {
+        constexpr int S0 = decltype(s)::value;
+        if constexpr (!kBetween)
+            convert(wb[0], S0);
 #pragma unroll
         for (int r = 0; r < T::kRows; ++r)
+            row_products(wb[kBetween ? S0 % 2 : 0], x, r);
+        if constexpr (kBetween) {
+            convert(wb[(S0 + 1) % 2], S0 + 1);
 #pragma unroll
-            for (int c = 0; c < T::kCols; ++c)
-                acc[r][c] = mfma_16x16x32(wb[c], __builtin_bit_cast(bf16x8, x[r]), acc[r][c]);
+            for (int i = 0; i < T::kRows * T::kCols; ++i) {
+                __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);              // matrix
+                __builtin_amdgcn_sched_group_barrier(0x002, 6 / T::kRows + 1, 0);   // vector
+            }
+        }
     };
     auto take_codes = [&](u32x4 (&q)[T::kCols], uint32_t (&s)[T::kCols]) {
 #pragma unroll
@@ -326,11 +349,11 @@ __global__ void __launch_bounds__(kTileWaves * 64, 2) k_mx4_linear_tile(Mx4Linea
             transpose_groups(wq[c]);
         }
     };
-    // One step.  It has no branches (but for a chunk's ragged last step), so that
-    // the order of reads and products written here is the order they run in.
-    // drain: the stages in flight are no longer NS.
+    // One step.  The order of reads, loads and products written here is the order
+    // they run in (what a chunk's ragged last step does more is branched around).
+    // drain: no more loads start, and those in flight are no longer NS steps'.
     auto step = [&](auto tail, auto drain) {
-        constexpr bool TAIL = decltype(tail)::value != 0;
+        constexpr bool TAIL = decltype(tail)::value != 0, DRAIN = decltype(drain)::value != 0;
         if constexpr (XMX) {
             read_x(xb, kHalf);
             __builtin_amdgcn_sched_barrier(0);
@@ -344,7 +367,11 @@ __global__ void __launch_bounds__(kTileWaves * 64, 2) k_mx4_linear_tile(Mx4Linea
                 for (int r = 0; r < kHalf; ++r)
                     acc[r][c] = mfma_mx4(w[c], xa[r], acc[r][c]);
             __builtin_amdgcn_sched_barrier(0);
-            next_step(tail, drain);
+            const uint32_t freed = next_step(tail, drain);
+            if constexpr (!DRAIN) {
+                unrolled<kStepLoads>([&](auto i) { load_piece(i, freed); });
+                end_loads();
+            }
             read_x(xa, 0);
             __builtin_amdgcn_sched_barrier(0);
             if constexpr (TAIL)
@@ -363,28 +390,42 @@ __global__ void __launch_bounds__(kTileWaves * 64, 2) k_mx4_linear_tile(Mx4Linea
         } else {
             read_block(odd, 1);
             __builtin_amdgcn_sched_barrier(0);
-            products(even, 0);
+            products(even, Flag<0>());
             __builtin_amdgcn_sched_barrier(0);
             read_block(even, 2);
             __builtin_amdgcn_sched_barrier(0);
             if (!TAIL || rem > 1)
-                products(odd, 1);
+                products(odd, Flag<1>());
             __builtin_amdgcn_sched_barrier(0);
             read_block(odd, 3);
             __builtin_amdgcn_sched_barrier(0);
             if (!TAIL || rem > 2)
-                products(even, 2);
+                products(even, Flag<2>());
             __builtin_amdgcn_sched_barrier(0);
-            next_step(tail, drain);
+            const uint32_t freed = next_step(tail, drain);
             u32x4 q[T::kCols];
             uint32_t s4[T::kCols];
             read_codes(q, s4);
             read_block(even, 0);
             __builtin_amdgcn_sched_barrier(0);
-            if constexpr (!TAIL)
-                products(odd, 3);
-            __builtin_amdgcn_sched_barrier(0);
+            if constexpr (!TAIL && !kBetween)
+                convert(wb[1], 3);
+            unrolled<T::kRows>([&](auto r) {
+                if constexpr (!TAIL)
+                    row_products(wb[1], odd, r.value);
+                __builtin_amdgcn_sched_barrier(0);
+                if constexpr (!DRAIN)
+                    unrolled<kStepLoads>([&](auto i) {
+                        if constexpr (i.value * T::kRows / kStepLoads == r.value)
+                            load_piece(i, freed);
+                    });
+                __builtin_amdgcn_sched_barrier(0);
+            });
+            if constexpr (!DRAIN)
+                end_loads();
             take_codes(q, s4);
+            if constexpr (kBetween)
+                convert(wb[0], 0);
         }
     };
 
@@ -398,17 +439,22 @@ __global__ void __launch_bounds__(kTileWaves * 64, 2) k_mx4_linear_tile(Mx4Linea
         uint32_t s4[T::kCols];
         read_codes(q, s4);
         take_codes(q, s4);
+        convert(wb[0], 0);
         read_block(even, 0);
     }
-    int full = steps - T::kStages + 1;       // steps with all the later stages in flight
+    int full = steps - T::kStages;           // steps that start loads
     for (int chunk = 0; chunk < chunks; ++chunk) {
         const int n = max(0, min(full, whole_steps));
         for (int t = 0; t < n; ++t)
             step(Flag<0>(), Flag<0>());
         for (int t = n; t < whole_steps; ++t)
             step(Flag<0>(), Flag<1>());
-        if (rem)
-            step(Flag<1>(), Flag<1>());
+        if (rem) {
+            if (full >= chunk_steps)
+                step(Flag<1>(), Flag<0>());
+            else
+                step(Flag<1>(), Flag<1>());
+        }
         full -= chunk_steps;
         if constexpr (SPLIT) {
 #pragma unroll
