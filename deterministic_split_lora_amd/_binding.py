@@ -5,7 +5,8 @@ takes torch tensors that already live on the GPU, checks dtypes and that rows
 are contiguous, passes raw pointers, row strides and sizes, and raises
 ``LoraError`` on a nonzero status.  Every step of the computation runs in the
 HIP kernels; there is no fallback.  torch is used only for device memory and
-the current stream.
+the current stream.  The operators around the adapters are marshalled by
+csrc/binding.cpp instead of ctypes.
 """
 from __future__ import annotations
 
@@ -547,42 +548,57 @@ def lora_sgmv_expand(h, B_ptrs, ranks, scales, token_adapter, n_adapters: int, y
 
 
 # ----------------------------------------------------------------------------
-# the operators around the adapters
+# the operators around the adapters: the same marshalling, compiled
+# (csrc/binding.cpp), because their small calls take less time on the GPU than
+# ctypes takes to pass their arguments
 # ----------------------------------------------------------------------------
-def _same_rows(rows, t, name):
-    if t.shape[0] != rows:
-        raise ValueError(f"{name} must have {rows} rows, got {t.shape[0]}")
+NATIVE_PATH = os.path.join(_HERE, "_native.so")
+_native_module = None
+_raw_stream = None
 
 
-def _mx4(q, scales, K, name):
-    """Checks one MX4 operand: codes [rows, K/2] and scales [rows, >= K/32], both uint8."""
-    import torch
-    _dtype(q, torch.uint8, name + " codes"); _dtype(scales, torch.uint8, name + " scales")
-    if q.dim() != 2 or scales.dim() != 2 or q.shape[1] * 2 != K or scales.shape[1] * 32 < K:
-        raise ValueError(f"{name}: codes must be [rows, {K // 2}] and scales [rows, at least {K // 32}]")
-    _same_rows(q.shape[0], scales, name + " scales")
+def _native():
+    """The compiled binding, bound to lib()'s entry points; raises ImportError when it has not been built."""
+    global _native_module, _raw_stream
+    if _native_module is None:
+        import importlib.util
+        import torch
+        if not os.path.exists(NATIVE_PATH):
+            raise ImportError(f"{NATIVE_PATH} is missing: build it with `python -m deterministic_split_lora_amd.build`")
+        spec = importlib.util.spec_from_file_location(__package__ + "._native", NATIVE_PATH)
+        m = importlib.util.module_from_spec(spec)
+        spec.loader.exec_module(m)
+        L = lib()
+        m.bind(*(ctypes.cast(getattr(L, name), _vp).value for name in (
+            "lora_mx4_quantize", "lora_mx4_dequantize", "lora_mx4_linear", "lora_mx4_linear_q", "lora_block_norm",
+            "lora_sample")))
+        # the current stream's address without building a Stream object
+        _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
+            lambda device: torch.cuda.current_stream(device).cuda_stream)
+        _native_module = m
+    return _native_module
+
+
+def _stream_address(stream, like):
+    if stream is None:
+        return _raw_stream(like.get_device()) if getattr(like, "is_cuda", False) else 0
+    return stream if isinstance(stream, int) else stream.cuda_stream
 
 
 def lora_mx4_quantize(x, q, scales, stream=None):
     """q, scales = MX4 codes and block scales of x's rows (x [M,K] bf16, q [M,K/2] uint8, scales uint8 of M rows
     with a row stride that is a multiple of 4)."""
-    import torch
-    _dtype(x, torch.bfloat16, "x")
-    M, K = x.shape
-    _mx4(q, scales, K, "x"); _same_rows(M, q, "q")
-    _check(lib().lora_mx4_quantize(_ptr(x), _ld(x, "x"), _ptr(q), _ld(q, "q"), _ptr(scales), _ld(scales, "scales"),
-                                   M, K, _stream(stream, x)), "lora_mx4_quantize")
+    st = (_native_module or _native()).mx4_quantize(x, q, scales, _stream_address(stream, x))
+    if st:
+        raise LoraError(st, "lora_mx4_quantize")
     return q, scales
 
 
 def lora_mx4_dequantize(q, scales, x, stream=None):
     """x = the values of MX4 codes and block scales, as bf16."""
-    import torch
-    _dtype(x, torch.bfloat16, "x")
-    M, K = x.shape
-    _mx4(q, scales, K, "x"); _same_rows(M, q, "q")
-    _check(lib().lora_mx4_dequantize(_ptr(q), _ld(q, "q"), _ptr(scales), _ld(scales, "scales"), _ptr(x), _ld(x, "x"),
-                                     M, K, _stream(stream, x)), "lora_mx4_dequantize")
+    st = (_native_module or _native()).mx4_dequantize(x, q, scales, _stream_address(stream, x))
+    if st:
+        raise LoraError(st, "lora_mx4_dequantize")
     return x
 
 
@@ -592,39 +608,22 @@ def lora_mx4_linear_workspace_bytes(M: int, K: int, N: int, split_k: int) -> int
 
 def lora_mx4_linear(x, wq, ws, y, split_k: int = 8, workspace=None, stream=None):
     """y = x @ W^T (x [M,K] bf16, W as MX4 codes wq [N,K/2] and scales ws, y [M,N] bf16); chunks of K / split_k are
-    summed on their own and added in order."""
-    import torch
-    _dtype(x, torch.bfloat16, "x"); _dtype(y, torch.bfloat16, "y")
-    M, K = x.shape
-    _mx4(wq, ws, K, "W"); _same_rows(M, y, "y"); _same_rows(y.shape[1], wq, "W")
-    _check(lib().lora_mx4_linear(_ptr(x), _ld(x, "x"), _ptr(wq), _ld(wq, "wq"), _ptr(ws), _ld(ws, "ws"), _ptr(y),
-                                 _ld(y, "y"), M, K, y.shape[1], split_k, _ptr(workspace), _nbytes(workspace),
-                                 _stream(stream, x)), "lora_mx4_linear")
+    summed on their own and added in order.  workspace: tensor of lora_mx4_linear_workspace_bytes, None if that is 0."""
+    st = (_native_module or _native()).mx4_linear(x, wq, ws, y, split_k, workspace, _stream_address(stream, x))
+    if st:
+        raise LoraError(st, "lora_mx4_linear")
     return y
 
 
 def lora_mx4_linear_q(xq, xs, wq, ws, y, split_k: int = 8, workspace=None, stream=None):
     """lora_mx4_linear with x as MX4 codes xq [M,K/2] and scales xs."""
-    import torch
-    _dtype(y, torch.bfloat16, "y")
-    M, K = xq.shape[0], 2 * xq.shape[1]
-    _mx4(xq, xs, K, "x"); _mx4(wq, ws, K, "W"); _same_rows(M, y, "y"); _same_rows(y.shape[1], wq, "W")
-    _check(lib().lora_mx4_linear_q(_ptr(xq), _ld(xq, "xq"), _ptr(xs), _ld(xs, "xs"), _ptr(wq), _ld(wq, "wq"),
-                                   _ptr(ws), _ld(ws, "ws"), _ptr(y), _ld(y, "y"), M, K, y.shape[1], split_k,
-                                   _ptr(workspace), _nbytes(workspace), _stream(stream, y)), "lora_mx4_linear_q")
+    st = (_native_module or _native()).mx4_linear_q(xq, xs, wq, ws, y, split_k, workspace, _stream_address(stream, y))
+    if st:
+        raise LoraError(st, "lora_mx4_linear_q")
     return y
 
 
 NORM_KINDS = {"none": 0, "rms": 1, "layer": 2}
-
-
-def _vector(t, n, dt, name):
-    """A contiguous 1-D GPU tensor of n elements, or None."""
-    if t is None:
-        return
-    _dtype(t, dt, name)
-    if t.dim() != 1 or t.shape[0] != n or not t.is_contiguous():
-        raise ValueError(f"{name} must be a contiguous vector of {n} elements")
 
 
 def lora_block_norm(r, r_out, y=None, post: str = "none", post_w=None, post_b=None, gate=None, gate_group=None,
@@ -633,47 +632,19 @@ def lora_block_norm(r, r_out, y=None, post: str = "none", post_w=None, post_b=No
     """r_out = res_scale * r + gate * post_norm(y), x_out = pre_norm of that (all [M,C] bf16).  post, pre: "none",
     "rms" or "layer".  gate [G,C]: row i // gate_group is used for row i (default: ceil(M / G), so one row for all
     or one for each)."""
-    import torch
-    bf16 = torch.bfloat16
-    M, C = r.shape
-    for name, t in (("r", r), ("r_out", r_out), ("y", y), ("x_out", x_out)):
-        if t is not None:
-            _dtype(t, bf16, name)
-            if t.shape != r.shape:
-                raise ValueError(f"{name} must be [{M}, {C}]")
-    for name, t in (("post_w", post_w), ("post_b", post_b), ("pre_w", pre_w), ("pre_b", pre_b)):
-        _vector(t, C, bf16, name)
-    group = 1
-    if gate is not None:
-        _dtype(gate, bf16, "gate")
-        if gate.dim() != 2 or gate.shape[1] != C or gate.shape[0] < 1:
-            raise ValueError(f"gate must be [rows, {C}]")
-        group = max(1, -(-M // gate.shape[0])) if gate_group is None else int(gate_group)
-        if group < 1 or gate.shape[0] * group < M:
-            raise ValueError(f"gate has {gate.shape[0]} rows for groups of {group}: {M} rows need more")
-    _check(lib().lora_block_norm(_ptr(y), 0 if y is None else _ld(y, "y"), NORM_KINDS[post], _ptr(post_w),
-                                 _ptr(post_b), _ptr(gate), 0 if gate is None else _ld(gate, "gate"), group, _ptr(r),
-                                 _ld(r, "r"), res_scale, _ptr(r_out), _ld(r_out, "r_out"), NORM_KINDS[pre],
-                                 _ptr(pre_w), _ptr(pre_b), _ptr(x_out), 0 if x_out is None else _ld(x_out, "x_out"),
-                                 M, C, eps, _stream(stream, r)), "lora_block_norm")
+    st = (_native_module or _native()).block_norm(y, NORM_KINDS[post], post_w, post_b, gate, gate_group, r, res_scale,
+                                                  r_out, NORM_KINDS[pre], pre_w, pre_b, x_out, eps,
+                                                  _stream_address(stream, r))
+    if st:
+        raise LoraError(st, "lora_block_norm")
     return r_out, x_out
 
 
 def lora_sample(logits, u, tokens, temperature=None, top_k=None, top_p=None, min_p=None, logprobs=None, stream=None):
     """tokens[i] drawn from row i of logits ([B,V] bf16 or fp32) with the random number u[i] in [0, 1), after
     temperature, top-k, top-p and min-p (vectors of B, None: off); logprobs[i]: log of its probability."""
-    import torch
-    f32, i32 = torch.float32, torch.int32
-    if logits.dtype not in (torch.bfloat16, f32):
-        raise TypeError(f"logits must be bfloat16 or float32, got {logits.dtype}")
-    _dtype(logits, logits.dtype, "logits")
-    ld = _ld(logits, "logits")
-    B, V = logits.shape
-    for name, t, dt in (("u", u, f32), ("tokens", tokens, i32), ("temperature", temperature, f32),
-                        ("top_k", top_k, i32), ("top_p", top_p, f32), ("min_p", min_p, f32),
-                        ("logprobs", logprobs, f32)):
-        _vector(t, B, dt, name)
-    _check(lib().lora_sample(_ptr(logits), 0 if logits.dtype == torch.bfloat16 else 1, ld, B, V, _ptr(temperature),
-                             _ptr(top_k), _ptr(top_p), _ptr(min_p), _ptr(u), _ptr(tokens), _ptr(logprobs),
-                             _stream(stream, logits)), "lora_sample")
+    st = (_native_module or _native()).sample(logits, temperature, top_k, top_p, min_p, u, tokens, logprobs,
+                                              _stream_address(stream, logits))
+    if st:
+        raise LoraError(st, "lora_sample")
     return tokens

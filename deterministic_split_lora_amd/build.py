@@ -1,4 +1,5 @@
-"""Builds liblora_det.so (the HIP kernels and the C entry points) for gfx950.
+"""Builds liblora_det.so (the HIP kernels and the C entry points) for gfx950,
+and _native.so (compiled argument marshalling for the package, host code).
 
 Run ``python -m deterministic_split_lora_amd.build`` or call ``build()``.  The
 library is written next to this file so it travels with the source tree.
@@ -12,6 +13,7 @@ import sys
 HERE = os.path.dirname(os.path.abspath(__file__))
 CSRC = os.path.join(HERE, "csrc")
 LIB = os.path.join(HERE, "liblora_det.so")
+BINDING = os.path.join(HERE, "_native.so")
 SOURCES = ["abi.hip", "shrink.hip", "expand.hip", "fused.hip", "streamed.hip", "sgmv_plan.hip",
            "abi_step.hip", "mx4.hip", "mx4_linear.hip", "block_norm.hip", "sample.hip"]
 HEADERS = ["device.h", "kernels.h", "shrink_tile.h", "step_kernels.h", "mx4.h"]
@@ -59,6 +61,18 @@ def _record_revision() -> None:
             f.write(rev + ("-dirty" if dirty else "") + "\n")
 
 
+def binding_command(out: str) -> list:
+    """The host compiler's line for csrc/binding.cpp, against the installed torch's headers."""
+    import sysconfig
+    import torch
+    from torch.utils import cpp_extension
+    include = ["-isystem" + i for i in cpp_extension.include_paths()] + ["-I" + sysconfig.get_paths()["include"]]
+    return ["g++", "-O2", "-std=c++17", "-fPIC", "-shared", "-fvisibility=hidden", "-Wall",
+            "-D_GLIBCXX_USE_CXX11_ABI=%d" % torch._C._GLIBCXX_USE_CXX11_ABI, *include,
+            os.path.join(CSRC, "binding.cpp"), "-o", out, "-L" + cpp_extension.library_paths()[0],
+            "-ltorch_python", "-ltorch_cpu", "-lc10"]
+
+
 def build(verbose: bool = False) -> str:
     """Compile every source; always recompiles (a cross-compile, no GPU needed).
     Each source is compiled to an object in parallel, then the objects are
@@ -81,13 +95,18 @@ def build(verbose: bool = False) -> str:
     try:
         jobs = [[hipcc(), *compile_flags, *inc, "-c", os.path.join(CSRC, s), "-o", o]
                 for s, o in zip(SOURCES, objs)]
+        native = BINDING + ".tmp" + tag
+        objs.append(native)                  # removed below if it is not put in place
+        jobs.append(binding_command(native))
         with ThreadPoolExecutor(max_workers=min(len(jobs), os.cpu_count() or 1)) as ex:
             results = list(ex.map(run, jobs))
         errs = "\n".join(e for _, e in results if e.strip())
         if any(rc != 0 for rc, _ in results):
-            raise RuntimeError("hipcc failed:\n" + errs)
+            raise RuntimeError("compilation failed:\n" + errs)
         if verbose and errs:
             print(errs, file=sys.stderr)
+        objs.remove(native)
+        os.replace(native, BINDING)
         tmp = LIB + ".tmp" + tag
         rc, err = run([hipcc(), "--offload-arch=gfx950", "-shared", "-fPIC", *objs, "-o", tmp])
         if rc != 0:
