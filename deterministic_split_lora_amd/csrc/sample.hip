@@ -345,8 +345,7 @@ struct Fast {
     uint32_t key[kList];
     uint32_t idx[kList];
     unsigned long long sub[kThreads];
-    uint32_t few_key[kFew];
-    uint32_t few_idx[kFew];
+    unsigned long long few[kFew];            // place() of an element
     uint32_t few_w[kFew];
     unsigned long long range[kWaves];
     uint64_t scan[2 * kWaves];
@@ -384,51 +383,132 @@ struct Groups {
 
     __device__ int first(int group) const { return group * kVec - off; }
 
-    // The group's logits; columns outside the row (never read) and NaN as -inf.
-    __device__ void load(int group, float (&l)[kVec]) const
+    // A group's 16 bytes, which lie in the row.
+    __device__ __forceinline__ u32x4 load(int group) const
     {
-        const int i0 = first(group);
-        if (i0 >= 0 && i0 + kVec <= V) {
-            const u32x4 v = *(const global_u32x4*)(base + (int64_t)group * 16);
+        return *(const global_u32x4*)(base + (int64_t)group * 16);
+    }
+
+    // The same of any group, element by element, with -inf outside the row (never
+    // read there).
+    __device__ __forceinline__ u32x4 load_edge(int group) const
+    {
+        u32x4 v = {0, 0, 0, 0};
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                if constexpr (BF16) {
-                    l[2 * e] = __builtin_bit_cast(float, v[e] << 16);
-                    l[2 * e + 1] = __builtin_bit_cast(float, v[e] & 0xFFFF0000u);
-                } else {
-                    const uint32_t b = v[e];
-                    l[e] = __builtin_bit_cast(float, b);
-                }
+        for (int e = 0; e < kVec; ++e) {
+            const int i = first(group) + e;
+            const bool in = i >= 0 && i < V;
+            if constexpr (BF16) {
+                const uint32_t b = in ? reinterpret_cast<const uint16_t*>(base)[(int64_t)group * kVec + e] : 0xFF80u;
+                v[e / 2] |= b << (16 * (e % 2));
+            } else {
+                v[e] = in ? reinterpret_cast<const uint32_t*>(base)[(int64_t)group * kVec + e] : 0xFF800000u;
             }
-        } else {
+        }
+        return v;
+    }
+
+    __device__ bool whole(int group) const { return first(group) >= 0 && first(group) + kVec <= V; }
+
+    // Its logits; NaN as -inf, -0 as +0.
+    static __device__ __forceinline__ void logits(u32x4 v, float (&l)[kVec])
+    {
 #pragma unroll
-            for (int e = 0; e < kVec; ++e) {
-                l[e] = -INFINITY;
-                if (i0 + e >= 0 && i0 + e < V) {
-                    if constexpr (BF16)
-                        l[e] = bf16_bits_to_f32(reinterpret_cast<const uint16_t*>(base)[(int64_t)group * kVec + e]);
-                    else
-                        l[e] = reinterpret_cast<const float*>(base)[(int64_t)group * kVec + e];
-                }
+        for (int e = 0; e < 4; ++e) {
+            const uint32_t b = v[e];
+            if constexpr (BF16) {
+                l[2 * e] = __builtin_bit_cast(float, b << 16);
+                l[2 * e + 1] = __builtin_bit_cast(float, b & 0xFFFF0000u);
+            } else {
+                l[e] = __builtin_bit_cast(float, b);
             }
         }
 #pragma unroll
         for (int e = 0; e < kVec; ++e)
             l[e] = l[e] != l[e] ? -INFINITY : l[e] + 0.0f;
     }
+
+    // f(logit, column) over this wave's run, with the loads of the next kAhead
+    // groups in flight; the row's first and last group may be cut and come last.
+    template <class F>
+    __device__ __forceinline__ void each(F f) const
+    {
+        constexpr int kAhead = 4;
+        const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63;
+        const int begin = max(wave * run, whole(0) ? 0 : 1);
+        const int end = min((wave + 1) * run, whole(n - 1) ? n : n - 1);
+        if (begin < end) {
+            u32x4 v[kAhead];
+#pragma unroll
+            for (int a = 0; a < kAhead; ++a) // past the run: its last group again
+                v[a] = load(min(begin + lane + a * 64, end - 1));
+#pragma unroll 1
+            for (int g = begin + lane; g - lane < end; g += 64) {
+                const u32x4 now = v[0];
+#pragma unroll
+                for (int a = 0; a + 1 < kAhead; ++a)
+                    v[a] = v[a + 1];
+                v[kAhead - 1] = load(min(g + kAhead * 64, end - 1));
+                if (g < end)
+                    apply(now, g, f);
+            }
+        }
+        // lane 0 has the first group, lane 1 the last, if they are cut
+        const int cut = lane == 0 ? 0 : n - 1;
+        if (lane < (n > 1 ? 2 : 1) && !whole(cut) && cut / run == wave)
+            apply(load_edge(cut), cut, f);
+    }
+
+    template <class F>
+    __device__ __forceinline__ void apply(u32x4 v, int g, F f) const
+    {
+        float l[kVec];
+        logits(v, l);
+#pragma unroll
+        for (int e = 0; e < kVec; ++e)
+            f(l[e], first(g) + e);
+    }
 };
 
-// Weight of a logit where the maximum and the inverse temperature are finite.
-__device__ __forceinline__ uint32_t weight_finite(const Row& r, float l)
+// Where the maximum and the inverse temperature are finite: the exponent of a
+// logit and the weight it gives.
+__device__ __forceinline__ float exponent(const Row& r, float l)
 {
-    return __float2uint_rn(expf((l - r.lmax) * r.inv_t) * kOne);
+    return (l - r.lmax) * r.inv_t;
 }
 
-// Bin of a logit: 0 at the maximum, rising as it falls; kHist - 1 for what
-// surely has no weight.  Monotonous, being rounded products and differences.
-__device__ __forceinline__ int weight_bin(const Row& r, float l)
+__device__ __forceinline__ uint32_t weight_of_exponent(float z)
 {
-    return (int)fminf((r.lmax - l) * r.inv_t * kBinsPerUnit, (float)(kHist - 1));
+    return __float2uint_rn(expf(z) * kOne);
+}
+
+__device__ __forceinline__ uint32_t weight_finite(const Row& r, float l)
+{
+    return weight_of_exponent(exponent(r, l));
+}
+
+// Place among the bins, whose number is its whole part: 0 at the maximum, rising
+// as the logit falls; kHist - 1 and above for what surely has no weight.
+// Monotonous, being rounded products and differences.
+__device__ __forceinline__ float bin_place(float z)
+{
+    return -z * kBinsPerUnit;
+}
+
+__device__ __forceinline__ int bin_of(float place)
+{
+    return (int)fminf(place, (float)(kHist - 1));
+}
+
+// An element's place in the order, as a number that falls along it.
+__device__ __forceinline__ uint64_t place(uint32_t key, int column)
+{
+    return (uint64_t)key << 32 | ~(uint32_t)column;
+}
+
+__device__ __forceinline__ uint32_t place_column(uint64_t place)
+{
+    return ~(uint32_t)place;
 }
 
 __device__ __forceinline__ float block_reduce_max(float v, float* buf)
@@ -463,30 +543,22 @@ __device__ __forceinline__ uint64_t block_sum(uint64_t v, uint64_t* buf)
     return v;
 }
 
-__device__ __forceinline__ bool comes_before(uint32_t ka, uint32_t ia, uint32_t kb, uint32_t ib)
-{
-    return ka > kb || (ka == kb && ia < ib);
-}
-
-// The few elements s.few_* [0, n): 1024 / size threads stand for each.  For this
-// thread's element sums f over the others j, threads of an element sharing them.
-template <class F>
-__device__ __forceinline__ void over_few(int n, F f)
-{
-    int share = kThreads;
-    while (share > 1 && (kThreads / share) < n)
-        share >>= 1;
-    const int part = threadIdx.x % share;
-    for (int j = part; j < n; j += share)
-        f(j);
-}
-
+// s.few[0, n) are compared with one another: few_share(n) neighbouring threads
+// stand for each element, and share the others among them.
 __device__ __forceinline__ int few_share(int n)
 {
     int share = kThreads;
     while (share > 1 && (kThreads / share) < n)
         share >>= 1;
     return share;
+}
+
+template <class F>
+__device__ __forceinline__ void over_few(int n, int share, F f)
+{
+#pragma unroll 4
+    for (int j = threadIdx.x % share; j < n; j += share)
+        f(j);
 }
 
 // Sum over the `share` neighbouring threads that stand for one element.
@@ -514,13 +586,12 @@ template <bool BF16>
 __device__ bool sample_top_k(const SampleParams& p, const Settings& c, const Row& r, const Groups<BF16>& G, Fast& s,
                              int64_t row, float mine)
 {
-    constexpr int kVec = Groups<BF16>::kVec;
     // bins over the maxima's range; a thread without logits has none
     const float lowest = -block_reduce_max(mine == -INFINITY ? -INFINITY : -mine, s.red);
     if (!(r.lmax - lowest < INFINITY))
         return false;
     const float per = lowest < r.lmax ? (kThreads - 1) / (r.lmax - lowest) : 0.0f;
-    auto bin = [&](float l) { return (int)fminf((r.lmax - l) * per, (float)kThreads); };
+    auto at = [&](float l) { return (r.lmax - l) * per; };
     uint32_t* count = reinterpret_cast<uint32_t*>(s.sub);
     count[threadIdx.x] = 0;
     if (threadIdx.x == 0) {
@@ -529,7 +600,7 @@ __device__ bool sample_top_k(const SampleParams& p, const Settings& c, const Row
     }
     __syncthreads();
     if (mine != -INFINITY)
-        atomicAdd(&count[min(bin(mine), kThreads - 1)], 1u);
+        atomicAdd(&count[(int)fminf(at(mine), (float)(kThreads - 1))], 1u);
     __syncthreads();
     const uint64_t own = count[threadIdx.x];
     const uint64_t upto = block_scan(own, s.scan);
@@ -537,38 +608,31 @@ __device__ bool sample_top_k(const SampleParams& p, const Settings& c, const Row
     if (enough)
         s.pick = threadIdx.x;
     __syncthreads();
-    const int last_bin = s.pick;
     // with fewer than k maxima the k-th logit may lie below all of them
     const bool all = block_sum(own, s.scan) < (uint64_t)c.k;
-    const int begin = (threadIdx.x >> 6) * G.run, end = min(G.n, begin + G.run);
-    for (int g = begin + (threadIdx.x & 63); g < end; g += 64) {
-        float l[kVec];
-        G.load(g, l);
-#pragma unroll
-        for (int e = 0; e < kVec; ++e) {
-            if (l[e] != -INFINITY && (all || bin(l[e]) <= last_bin)) {
-                const uint32_t at = atomicAdd(&s.n, 1u);
-                if (at < kFew) {
-                    s.few_key[at] = order_key(l[e]);
-                    s.few_idx[at] = (uint32_t)(G.first(g) + e);
-                    s.few_w[at] = weight_finite(r, l[e]);
-                }
+    const float end_place = all ? INFINITY : (float)(s.pick + 1);
+    G.each([&](float l, int i) {
+        if (at(l) < end_place) {             // so is not -inf
+            const uint32_t slot = atomicAdd(&s.n, 1u);
+            if (slot < kFew) {
+                s.few[slot] = place(order_key(l), i);
+                s.few_w[slot] = weight_finite(r, l);
             }
         }
-    }
+    });
     __syncthreads();
     const int n = (int)s.n;
     if (n > kFew)
         return false;
     const int share = few_share(n), me = threadIdx.x / share;
-    const uint32_t key = me < n ? s.few_key[me] : 0, idx = me < n ? s.few_idx[me] : 0, w = me < n ? s.few_w[me] : 0;
+    const uint64_t mine_at = me < n ? s.few[me] : 0;
+    const uint32_t w = me < n ? s.few_w[me] : 0;
     uint64_t rank = 0, before = 0;
     if (me < n)
-        over_few(n, [&](int j) {
-            if (comes_before(s.few_key[j], s.few_idx[j], key, idx)) {
-                ++rank;
-                before += s.few_w[j];
-            }
+        over_few(n, share, [&](int j) {
+            const bool first = s.few[j] > mine_at;
+            rank += first;
+            before += first ? s.few_w[j] : 0u;
         });
     rank = share_sum(rank, share, s.scan);
     __syncthreads();
@@ -582,8 +646,9 @@ __device__ bool sample_top_k(const SampleParams& p, const Settings& c, const Row
         s.few_w[me] = keep ? w : 0;
     __syncthreads();
     uint64_t below = 0;                      // kept weight at lower indices
+    const uint32_t idx = place_column(mine_at);
     if (keep)
-        over_few(n, [&](int j) { below += s.few_idx[j] < idx ? s.few_w[j] : 0u; });
+        over_few(n, share, [&](int j) { below += place_column(s.few[j]) < idx ? s.few_w[j] : 0u; });
     below = share_sum(below, share, s.scan);
     const uint64_t t = target(c.u, total);
     if (lead && keep && below <= t && t < below + w)
@@ -600,20 +665,13 @@ __device__ bool sample_mass(const SampleParams& p, const Settings& c, const Row&
 {
     constexpr int kVec = Groups<BF16>::kVec;
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-    const int begin = wave * G.run, end = min(G.n, begin + G.run);
     const bool cut = c.top_p < 1.0f || c.floor_w > 0;
-    // the kept prefix ends with (key, last); floor_w applies on top
-    uint32_t key = 0, last = 0xFFFFFFFFu;
+    // the kept prefix ends with `last`; floor_w applies on top
+    uint64_t last = 0;
     uint64_t total = 0;
     if (!cut) {
         uint64_t sum = 0;
-        for (int g = begin + lane; g < end; g += 64) {
-            float l[kVec];
-            G.load(g, l);
-#pragma unroll
-            for (int e = 0; e < kVec; ++e)
-                sum += weight_finite(r, l[e]);
-        }
+        G.each([&](float l, int) { sum += weight_finite(r, l); });
 #pragma unroll
         for (int d = 1; d < 64; d <<= 1)
             sum += __shfl_xor((unsigned long long)sum, d);
@@ -628,16 +686,12 @@ __device__ bool sample_mass(const SampleParams& p, const Settings& c, const Row&
             s.lo = 0xFFFFFFFFu;
             s.hi = 0;
         }
-        for (int g = begin + lane; g < end; g += 64) {
-            float l[kVec];
-            G.load(g, l);
-#pragma unroll
-            for (int e = 0; e < kVec; ++e) {
-                const uint32_t w = weight_finite(r, l[e]);
-                if (w)
-                    atomicAdd(&s.hist[wave][weight_bin(r, l[e])], (unsigned long long)w);
-            }
-        }
+        G.each([&](float l, int) {
+            const float z = exponent(r, l);
+            const uint32_t w = weight_of_exponent(z);
+            if (w)
+                atomicAdd(&s.hist[wave][bin_of(bin_place(z))], (unsigned long long)w);
+        });
         __syncthreads();
         // the bin where top-p cuts
         uint64_t own = 0;
@@ -670,34 +724,30 @@ __device__ bool sample_mass(const SampleParams& p, const Settings& c, const Row&
             }
         }
         // bins below `from` are kept whole, bins above `to` not at all
-        for (int g = begin + lane; g < end; g += 64) {
-            float l[kVec];
-            G.load(g, l);
-#pragma unroll
-            for (int e = 0; e < kVec; ++e) {
-                const int b = weight_bin(r, l[e]);
-                if (b >= from && b <= to && l[e] != -INFINITY) {
-                    const uint32_t at = atomicAdd(&s.n, 1u);
-                    if (at < kList) {
-                        s.key[at] = order_key(l[e]);
-                        s.idx[at] = (uint32_t)(G.first(g) + e);
-                    }
+        const float first_place = (float)from, end_place = to >= kHist - 1 ? INFINITY : (float)(to + 1);
+        G.each([&](float l, int i) {
+            const float at = bin_place(exponent(r, l));
+            if (at >= first_place && at < end_place) {         // so is not -inf
+                const uint32_t slot = atomicAdd(&s.n, 1u);
+                if (slot < kList) {
+                    s.key[slot] = order_key(l);
+                    s.idx[slot] = (uint32_t)i;
                 }
             }
-        }
+        });
         __syncthreads();
         const int n = (int)s.n;
         if (n > kList)
             return false;
-        auto weight_of = [&](uint32_t k) {
+        auto exponent_of = [&](uint32_t k) {
             const uint32_t b = k ^ ((k >> 31) ? 0x80000000u : 0xFFFFFFFFu);
-            return weight_finite(r, __builtin_bit_cast(float, b));
+            return exponent(r, __builtin_bit_cast(float, b));
         };
+        auto weight_of = [&](uint32_t k) { return weight_of_exponent(exponent_of(k)); };
         if (c.top_p < 1.0f && pick <= to) {
             // where in its bin: sub-bins over the bin's keys
             for (int i = threadIdx.x; i < n; i += kThreads) {
-                const uint32_t b = s.key[i] ^ ((s.key[i] >> 31) ? 0x80000000u : 0xFFFFFFFFu);
-                if (weight_bin(r, __builtin_bit_cast(float, b)) == pick) {
+                if (bin_of(bin_place(exponent_of(s.key[i]))) == pick) {
                     atomicMin(&s.lo, s.key[i]);
                     atomicMax(&s.hi, s.key[i]);
                 }
@@ -728,8 +778,7 @@ __device__ bool sample_mass(const SampleParams& p, const Settings& c, const Row&
                 if (k >= lo && k <= hi && (int)((hi - k) >> shift) == sub) {
                     const uint32_t at = atomicAdd(&s.n, 1u);
                     if (at < kFew) {
-                        s.few_key[at] = k;
-                        s.few_idx[at] = s.idx[i];
+                        s.few[at] = place(k, (int)s.idx[i]);
                         s.few_w[at] = weight_of(k);
                     }
                 }
@@ -740,20 +789,15 @@ __device__ bool sample_mass(const SampleParams& p, const Settings& c, const Row&
                 return false;
             const int share = few_share(m), me = threadIdx.x / share;
             uint64_t before = 0;
+            const uint64_t mine_at = me < m ? s.few[me] : 0;
             if (me < m)
-                over_few(m, [&](int j) {
-                    if (comes_before(s.few_key[j], s.few_idx[j], s.few_key[me], s.few_idx[me]))
-                        before += s.few_w[j];
-                });
+                over_few(m, share, [&](int j) { before += s.few[j] > mine_at ? s.few_w[j] : 0u; });
             before = share_sum(before, share, s.scan) + sub_before;
             // the last one kept: its predecessors stay below the mass, with it they reach it
-            if (me < m && threadIdx.x % share == 0 && before < mass && before + s.few_w[me] >= mass) {
-                s.lo = s.few_key[me];
-                s.hi = s.few_idx[me];
-            }
+            if (me < m && threadIdx.x % share == 0 && before < mass && before + s.few_w[me] >= mass)
+                s.sub[0] = mine_at;
             __syncthreads();
-            key = s.lo;
-            last = s.hi;
+            last = s.sub[0];
         }
         // kept weight of each range of indices
         if (threadIdx.x < kWaves)
@@ -768,7 +812,7 @@ __device__ bool sample_mass(const SampleParams& p, const Settings& c, const Row&
         }
         for (int i = threadIdx.x; i < n; i += kThreads) {
             const uint32_t k = s.key[i], w = weight_of(k);
-            if (w >= c.floor_w && (k > key || (k == key && s.idx[i] <= last)))
+            if (w >= c.floor_w && place(k, (int)s.idx[i]) >= last)
                 atomicAdd(&s.range[((int)s.idx[i] + G.off) / kVec / G.run], (unsigned long long)w);
         }
         __syncthreads();
@@ -789,13 +833,13 @@ __device__ bool sample_mass(const SampleParams& p, const Settings& c, const Row&
     const int first = range * G.run + threadIdx.x * per;
     const int stop = min(min(first + per, (range + 1) * G.run), G.n);
     auto kept = [&](float l, int i) -> uint32_t {
-        const uint32_t k = order_key(l), w = weight_finite(r, l);
-        return w >= c.floor_w && (k > key || (k == key && (uint32_t)i <= last)) ? w : 0u;
+        const uint32_t w = weight_finite(r, l);
+        return w >= c.floor_w && place(order_key(l), i) >= last ? w : 0u;
     };
     uint64_t own = 0;
     for (int g = first; g < stop; ++g) {
         float l[kVec];
-        G.load(g, l);
+        G.logits(G.whole(g) ? G.load(g) : G.load_edge(g), l);
 #pragma unroll
         for (int e = 0; e < kVec; ++e)
             own += kept(l[e], G.first(g) + e);
@@ -804,7 +848,7 @@ __device__ bool sample_mass(const SampleParams& p, const Settings& c, const Row&
     if (at <= t && t < at + own) {
         for (int g = first; g < stop; ++g) {
             float l[kVec];
-            G.load(g, l);
+            G.logits(G.whole(g) ? G.load(g) : G.load_edge(g), l);
 #pragma unroll
             for (int e = 0; e < kVec; ++e) {
                 const uint32_t w = kept(l[e], G.first(g) + e);
@@ -831,25 +875,39 @@ __global__ void __launch_bounds__(kThreads) k_sample(SampleParams p)
     const bool greedy = !(T > 0.0f);
     r.inv_t = greedy ? 1.0f : 1.0f / T;
     Settings c;
-    c.k = greedy ? 1 : (p.top_k ? p.top_k[row] : 0);
+    c.k = p.top_k ? p.top_k[row] : 0;
     c.k = c.k > 0 && c.k < p.V ? c.k : 0;
-    c.top_p = greedy || !p.top_p ? 1.0f : fminf(p.top_p[row], 1.0f);       // NaN: 1
-    const float min_p = greedy || !p.min_p ? 0.0f : p.min_p[row];
+    c.top_p = p.top_p ? fminf(p.top_p[row], 1.0f) : 1.0f;      // NaN: 1
+    const float min_p = p.min_p ? p.min_p[row] : 0.0f;
     c.floor_w = min_p > 0.0f ? (uint32_t)fmin(ceil((double)min_p * (double)kOne), (double)kOne) : 0u;
     c.u = p.u[row];
 
     const Groups<BF16> G(r.logits, r.V);
-    float mine = -INFINITY;
-    {
-        const int begin = (threadIdx.x >> 6) * G.run, end = min(G.n, begin + G.run);
-        for (int g = begin + (threadIdx.x & 63); g < end; g += 64) {
-            float l[Groups<BF16>::kVec];
-            G.load(g, l);
+    if (greedy) {                            // the first of the order
+        float best = -INFINITY;
+        int at = 0;
+        G.each([&](float l, int i) {
+            at = l > best || (l == best && i < at) ? i : at;
+            best = fmaxf(best, l);
+        });
+        uint64_t top = best == -INFINITY ? 0 : place(order_key(best), at);
 #pragma unroll
-            for (int e = 0; e < Groups<BF16>::kVec; ++e)
-                mine = fmaxf(mine, l[e]);
+        for (int d = 1; d < 64; d <<= 1)
+            top = max(top, (uint64_t)__shfl_xor((unsigned long long)top, d));
+        if ((threadIdx.x & 63) == 0)
+            s.scan[threadIdx.x >> 6] = top;
+        __syncthreads();
+        if (threadIdx.x == 0) {
+            for (int i = 1; i < kWaves; ++i)
+                top = max(top, s.scan[i]);
+            p.tokens[row] = top ? (int)place_column(top) : -1;
+            if (p.logprobs)
+                p.logprobs[row] = top ? 0.0f : -INFINITY;
         }
+        return;
     }
+    float mine = -INFINITY;
+    G.each([&](float l, int) { mine = fmaxf(mine, l); });
     r.lmax = block_reduce_max(mine, s.red);
     if (r.lmax == -INFINITY) {               // every logit masked
         if (threadIdx.x == 0) {
