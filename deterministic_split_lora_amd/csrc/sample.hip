@@ -39,9 +39,10 @@ __device__ __forceinline__ float logit(const Row& r, int i)
     return l != l ? -INFINITY : l + 0.0f;
 }
 
+// Orders like the logit (-0 with +0).
 __device__ __forceinline__ uint32_t order_key(float l)
 {
-    const uint32_t u = __builtin_bit_cast(uint32_t, l);
+    const uint32_t u = __builtin_bit_cast(uint32_t, l + 0.0f);
     return u ^ ((u >> 31) ? 0xFFFFFFFFu : 0x80000000u);
 }
 
@@ -410,7 +411,8 @@ struct Groups {
 
     __device__ bool whole(int group) const { return first(group) >= 0 && first(group) + kVec <= V; }
 
-    // Its logits; NaN as -inf, -0 as +0.
+    // Its logits as they are: a NaN compares false, is no maximum and has no
+    // weight, and order_key takes -0 as +0.
     static __device__ __forceinline__ void logits(u32x4 v, float (&l)[kVec])
     {
 #pragma unroll
@@ -423,15 +425,12 @@ struct Groups {
                 l[e] = __builtin_bit_cast(float, b);
             }
         }
-#pragma unroll
-        for (int e = 0; e < kVec; ++e)
-            l[e] = l[e] != l[e] ? -INFINITY : l[e] + 0.0f;
     }
 
-    // f(logit, column) over this wave's run, with the loads of the next kAhead
-    // groups in flight; the row's first and last group may be cut and come last.
+    // f(logits, first column) over the groups of this wave's run, with the loads of
+    // the next kAhead in flight; the row's first and last group may be cut and come last.
     template <class F>
-    __device__ __forceinline__ void each(F f) const
+    __device__ __forceinline__ void each_group(F f) const
     {
         constexpr int kAhead = 4;
         const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63;
@@ -449,24 +448,56 @@ struct Groups {
                 for (int a = 0; a + 1 < kAhead; ++a)
                     v[a] = v[a + 1];
                 v[kAhead - 1] = load(min(g + kAhead * 64, end - 1));
-                if (g < end)
-                    apply(now, g, f);
+                if (g < end) {
+                    float l[kVec];
+                    logits(now, l);
+                    f(l, first(g));
+                }
             }
         }
         // lane 0 has the first group, lane 1 the last, if they are cut
         const int cut = lane == 0 ? 0 : n - 1;
-        if (lane < (n > 1 ? 2 : 1) && !whole(cut) && cut / run == wave)
-            apply(load_edge(cut), cut, f);
+        if (lane < (n > 1 ? 2 : 1) && !whole(cut) && cut / run == wave) {
+            float l[kVec];
+            logits(load_edge(cut), l);
+            f(l, first(cut));
+        }
     }
 
+    // f(logit, column) over its elements
     template <class F>
-    __device__ __forceinline__ void apply(u32x4 v, int g, F f) const
+    __device__ __forceinline__ void each(F f) const
     {
-        float l[kVec];
-        logits(v, l);
+        each_group([&](float (&l)[kVec], int i0) {
 #pragma unroll
-        for (int e = 0; e < kVec; ++e)
-            f(l[e], first(g) + e);
+            for (int e = 0; e < kVec; ++e)
+                f(l[e], i0 + e);
+        });
+    }
+
+    // Puts the elements with take(logit) into a list by put(slot, logit, column);
+    // *n counts them.  A lane takes its slots once a group.
+    template <class T, class P>
+    __device__ __forceinline__ void gather(uint32_t* n, T take, P put) const
+    {
+        each_group([&](float (&l)[kVec], int i0) {
+            uint32_t hits = 0;
+#pragma unroll
+            for (int e = 0; e < kVec; ++e)
+                hits |= (uint32_t)take(l[e]) << e;
+            if (hits) {
+                uint32_t slot = atomicAdd(n, (uint32_t)__builtin_popcount(hits));
+#pragma unroll 1
+                for (; hits; hits &= hits - 1) {
+                    const int e = __builtin_ctz(hits);
+                    float v = l[0];
+#pragma unroll
+                    for (int j = 1; j < kVec; ++j)
+                        v = e == j ? l[j] : v;
+                    put(slot++, v, i0 + e);
+                }
+            }
+        });
     }
 };
 
@@ -611,15 +642,14 @@ __device__ bool sample_top_k(const SampleParams& p, const Settings& c, const Row
     // with fewer than k maxima the k-th logit may lie below all of them
     const bool all = block_sum(own, s.scan) < (uint64_t)c.k;
     const float end_place = all ? INFINITY : (float)(s.pick + 1);
-    G.each([&](float l, int i) {
-        if (at(l) < end_place) {             // so is not -inf
-            const uint32_t slot = atomicAdd(&s.n, 1u);
+    G.gather(
+        &s.n, [&](float l) { return at(l) < end_place; },      // so is not -inf
+        [&](uint32_t slot, float l, int i) {
             if (slot < kFew) {
                 s.few[slot] = place(order_key(l), i);
                 s.few_w[slot] = weight_finite(r, l);
             }
-        }
-    });
+        });
     __syncthreads();
     const int n = (int)s.n;
     if (n > kFew)
@@ -725,16 +755,18 @@ __device__ bool sample_mass(const SampleParams& p, const Settings& c, const Row&
         }
         // bins below `from` are kept whole, bins above `to` not at all
         const float first_place = (float)from, end_place = to >= kHist - 1 ? INFINITY : (float)(to + 1);
-        G.each([&](float l, int i) {
-            const float at = bin_place(exponent(r, l));
-            if (at >= first_place && at < end_place) {         // so is not -inf
-                const uint32_t slot = atomicAdd(&s.n, 1u);
+        G.gather(
+            &s.n,
+            [&](float l) {                   // so is not -inf
+                const float at = bin_place(exponent(r, l));
+                return at >= first_place && at < end_place;
+            },
+            [&](uint32_t slot, float l, int i) {
                 if (slot < kList) {
                     s.key[slot] = order_key(l);
                     s.idx[slot] = (uint32_t)i;
                 }
-            }
-        });
+            });
         __syncthreads();
         const int n = (int)s.n;
         if (n > kList)
