@@ -449,12 +449,14 @@ __global__ void __launch_bounds__(kTileWaves * 64, 2) k_mx4_linear_tile(Mx4Linea
             step(Flag<0>(), Flag<0>());
         for (int t = n; t < whole_steps; ++t)
             step(Flag<0>(), Flag<1>());
-        if (rem) {
-            if (full >= chunk_steps)
-                step(Flag<1>(), Flag<0>());
-            else
-                step(Flag<1>(), Flag<1>());
-        }
+        // several chunks whose scales come by the word are multiples of 128
+        if constexpr (MODE == kOneChunk || kUnit == 4)
+            if (rem) {
+                if (full >= chunk_steps)
+                    step(Flag<1>(), Flag<0>());
+                else
+                    step(Flag<1>(), Flag<1>());
+            }
         full -= chunk_steps;
         if constexpr (SPLIT) {
 #pragma unroll
@@ -489,18 +491,25 @@ __global__ void __launch_bounds__(kTileWaves * 64, 2) k_mx4_linear_tile(Mx4Linea
     }
 }
 
-template <bool XMX, int TM, int TN, TileMode MODE>
-hipError_t launch_tile(const Mx4LinearParams& p, hipStream_t st)
+template <bool XMX, int TM, int TN, TileMode MODE, int kUnit>
+hipError_t launch_tile_unit(const Mx4LinearParams& p, hipStream_t st)
 {
     const int64_t tiles = ((p.M + TM - 1) / TM) * ((p.N + TN - 1) / TN);
     const dim3 grid((unsigned)tiles, MODE == kPartial ? (unsigned)p.split_k : 1u), block(kTileWaves * 64);
+    hipLaunchKernelGGL((k_mx4_linear_tile<XMX, TM, TN, MODE, kUnit>), grid, block, 0, st, p);
+    return hipGetLastError();
+}
+
+template <bool XMX, int TM, int TN, TileMode MODE>
+hipError_t launch_tile(const Mx4LinearParams& p, hipStream_t st)
+{
     const uintptr_t rows = reinterpret_cast<uintptr_t>(p.ws) | (uintptr_t)p.ld_ws |
                            (XMX ? reinterpret_cast<uintptr_t>(p.xs) | (uintptr_t)p.ld_xs : 0);
     if (rows % 16 == 0 && (p.split_k == 1 || p.k_chunk % 128 == 0))
-        hipLaunchKernelGGL((k_mx4_linear_tile<XMX, TM, TN, MODE, 16>), grid, block, 0, st, p);
-    else
-        hipLaunchKernelGGL((k_mx4_linear_tile<XMX, TM, TN, MODE, 4>), grid, block, 0, st, p);
-    return hipGetLastError();
+        return launch_tile_unit<XMX, TM, TN, MODE, 16>(p, st);
+    // totals beside the sums and ragged chunks: the wide tile has no registers left
+    constexpr int kTN = MODE == kAllChunks && TN == 256 ? 128 : TN;
+    return launch_tile_unit<XMX, TM, kTN, MODE, 4>(p, st);
 }
 
 }  // namespace lora
