@@ -306,8 +306,9 @@ hipError_t launch_split_tile(const Mx4LinearParams& p, hipStream_t st)
 // split_k) and are within about 15% of them:
 //   rows    a chain's steps of 128 k follow one another, and a CU shares its waves'
 //           loads: by tiles of 16 tokens, one step alone / per CU
-//   tiles   a workgroup a CU, steps of 128 k one after another
-//   split   the smallest tiles, a chunk a workgroup, then the joining launch, which
+//   tiles   a workgroup a CU (two of the small tiles), steps of 128 k one after
+//           another
+//   split   the small tiles, a chunk a workgroup, then the joining launch, which
 //           moves 8 bytes an output and chunk
 // e.g. bf16 x, 200 x 4096 x 6144, split_k 4: 64 x 128 tiles 24.7 us, split 31, rows
 // 85, 128 x 256 tiles 56; 33 x 14336 x 4096, split_k 8: split 17.7, rows 36.5.
@@ -338,16 +339,20 @@ Schedule schedule_for(int64_t M, int64_t N, int32_t k_chunk, int32_t split_k, bo
             best = s;
         }
     };
-    auto rounds = [&](int64_t tm, int64_t tn, int64_t copies) {
-        return ceil_div(ceil_div(M, tm) * ceil_div(N, tn) * copies, kCus);
+    auto rounds = [&](int64_t tm, int64_t tn) { return ceil_div(ceil_div(M, tm) * ceil_div(N, tn), kCus); };
+    // the small tiles: two of them share a CU
+    const int64_t small_tiles = ceil_div(M, mx ? 128 : 64) * ceil_div(N, 128);
+    auto small = [&](int64_t copies) {
+        const int64_t n = small_tiles * copies, rest = n % (2 * kCus);
+        const int64_t alone1 = mx ? 520 : 770, paired = mx ? 700 : 900;
+        return n / (2 * kCus) * paired + (rest > kCus ? paired : rest > 0 ? alone1 : 0);
     };
-    const int64_t tm = mx ? 128 : 64, small = mx ? 520 : 740;
-    consider(kTileSmall, 2000 + rounds(tm, 128, 1) * steps * small);
-    consider(kTileMiddle, 2000 + rounds(128, 256, 1) * steps * (mx ? 720 : split_k > 1 ? 1700 : 1530));
+    consider(kTileSmall, 2000 + small(1) * steps);
+    consider(kTileMiddle, 2000 + rounds(128, 256) * steps * (mx ? 720 : split_k > 1 ? 1650 : 1530));
     if (mx && split_k == 1)
-        consider(kTileLarge, 2000 + rounds(256, 256, 1) * steps * 1100);
+        consider(kTileLarge, 2000 + rounds(256, 256) * steps * 1100);
     if (split_k > 1)
-        consider(kSplit, 6500 + rounds(tm, 128, split_k) * chunk_steps * small + M * N * split_k * 8 / 4000);
+        consider(kSplit, 6500 + small(split_k) * chunk_steps + M * N * split_k * 8 / 4500);
     return best;
 }
 
