@@ -303,7 +303,7 @@ hipError_t launch_split_tile(const Mx4LinearParams& p, hipStream_t st)
 
 // Which kernel a call takes: the one of least estimated time.  The estimates, in
 // ns, come from measurements on MI355X (K, N of 4096 .. 28672, M of 1 .. 4096, every
-// split_k) and are within about 15% of them:
+// split_k) and are within about 20% of them:
 //   rows    a chain's steps of 128 k follow one another, and a CU shares its waves'
 //           loads: by tiles of 16 tokens, one step alone / per CU
 //   tiles   a workgroup a CU (two of the small tiles), steps of 128 k one after
@@ -344,13 +344,13 @@ Schedule schedule_for(int64_t M, int64_t N, int32_t k_chunk, int32_t split_k, bo
     const int64_t small_tiles = ceil_div(M, mx ? 128 : 64) * ceil_div(N, 128);
     auto small = [&](int64_t copies) {
         const int64_t n = small_tiles * copies, rest = n % (2 * kCus);
-        const int64_t alone1 = mx ? 520 : 770, paired = mx ? 700 : 900;
+        const int64_t alone1 = mx ? 520 : 770, paired = mx ? 900 : 1100;
         return n / (2 * kCus) * paired + (rest > kCus ? paired : rest > 0 ? alone1 : 0);
     };
     consider(kTileSmall, 2000 + small(1) * steps);
-    consider(kTileMiddle, 2000 + rounds(128, 256) * steps * (mx ? 720 : split_k > 1 ? 1650 : 1530));
+    consider(kTileMiddle, 2000 + rounds(128, 256) * steps * (mx ? 790 : split_k > 1 ? 1750 : 1650));
     if (mx && split_k == 1)
-        consider(kTileLarge, 2000 + rounds(256, 256) * steps * 1100);
+        consider(kTileLarge, 2000 + rounds(256, 256) * steps * 1200);
     if (split_k > 1)
         consider(kSplit, 6500 + small(split_k) * chunk_steps + M * N * split_k * 8 / 4500);
     return best;

@@ -186,7 +186,8 @@ SIZES = [  # M, K, N, split_k
     (64, 14336, 128, 8), (65, 1024, 328, 1), (97, 640, 136, 4), (128, 2048, 512, 8), (129, 512, 776, 16),
     (200, 4096, 384, 4), (255, 1024, 264, 1), (256, 288, 1032, 1), (257, 1536, 520, 2), (300, 544, 136, 1),
     (511, 2048, 248, 8), (513, 192, 2056, 1), (1030, 1024, 1288, 1), (1100, 352, 776, 1), (700, 1056, 2304, 1),
-    (1025, 768, 2056, 4),
+    (1025, 768, 2056, 4), (1100, 256, 6144, 1), (1100, 256, 6144, 2), (1100, 320, 6144, 2), (1300, 416, 6144, 1),
+    (1300, 512, 6144, 1), (33, 2048, 1024, 16), (48, 3584, 512, 16), (64, 8192, 40, 1), (1, 16384, 24, 2),
 ]
 
 
@@ -533,6 +534,62 @@ def test_sample_edges(bf16):
     assert logprobs[1] == 0.0 and logprobs[6] == 0.0 and abs(logprobs[4] - np.log(0.5)) < 1e-6
 
 
+@pytest.mark.parametrize("bf16", [False, True])
+def test_sample_rows_of_every_path(bf16):
+    """top-k past what is gathered in one list, cuts near the smallest weights, logits from one end of the type to the
+    other, bins with more elements than their list holds."""
+    rng = rng_for(77, "paths")
+    V = 60000
+    rows, kw = [], dict(temperature=[], top_k=[], top_p=[], min_p=[])
+
+    def add(l, T=1.0, k=0, p=1.0, m=0.0):
+        rows.append(l)
+        for name, v in zip(kw, (T, k, p, m)):
+            kw[name].append(v)
+
+    base = rng.standard_normal(V) * 2.0
+    add(base, k=1024)
+    add(base, k=1025)
+    add(base, k=20000)
+    add(base, k=59999)
+    add(base, m=1e-9, T=0.25)
+    add(base, m=2.0 ** -31)
+    add(base, m=0.9)
+    wide = base.copy()
+    wide[:3] = [3.0e38, -3.0e38, -3.3e38]
+    add(wide, k=2)
+    add(wide, T=1e38)
+    add(wide, T=1e-39)                                         # its inverse is infinite
+    near = 1.0 + 2.0 ** -6 * rng.integers(0, 4, V)             # four values, all in few bins
+    add(near, k=30000)
+    few = base.copy()
+    few[rng.permutation(V)[:V - 40]] = -np.inf                 # forty tokens left
+    add(few, k=50)
+    add(few, k=39, T=2.0)
+    g, val = gpu_logits(np.stack(rows), bf16, pad=1)
+    want, u = [], []
+    for i in range(len(rows)):
+        kept = step.kept_weights(val[i], np.float32(kw["temperature"][i]), kw["top_k"][i], kw["top_p"][i], kw["min_p"][i])
+        if kw["temperature"][i] < 1e-38:                       # the maximum's elements share the weight
+            kept = (val[i] == val[i].max()).astype(np.int64) << 31
+        tok, x = steady(kept, rng)
+        want.append(tok)
+        u.append(x)
+    tokens, _ = run_sample(g, u, **kw)
+    assert tokens.tolist() == want
+
+
+def test_sample_largest_vocabulary():
+    V = 1 << 22
+    l = rng_for(5, "large").standard_normal((1, V)) * 3.0
+    g, val = gpu_logits(l, False)
+    for kw in (dict(), dict(temperature=[0.8], top_k=[7])):
+        kept = step.kept_weights(val[0], kw.get("temperature", [1.0])[0], kw.get("top_k", [0])[0])
+        tok, u = steady(kept, rng_for(6, "u"))
+        tokens, _ = run_sample(g, [u], **kw)
+        assert tokens[0] == tok
+
+
 def test_sample_large_ties_with_top_p():
     """Thousands of equal logits below a few large ones: the threshold falls inside the tie."""
     V = 100000
@@ -623,6 +680,13 @@ def test_operators_on_another_stream_and_in_a_graph():
         t.cuda.synchronize()
         for k in eager:
             assert t.equal(eager[k].view(t.uint8), captured[k].view(t.uint8)), f"replay {i}: {k}"
+
+
+def test_example_runs():
+    import examples.adapted_step as example
+    report = example.main(["--layers", "2", "--tokens", "5"])
+    assert report["tokens"] == report["reference_tokens"]
+    assert report["worst"] < 0.05
 
 
 def test_binding_refuses():

@@ -134,6 +134,18 @@ def test_sample_refusals(kw, status):
     assert sample(**kw) == status
 
 
+def test_compiled_binding_refuses_host_tensors():
+    import torch
+    x, q, s = torch.zeros(2, 64, dtype=torch.bfloat16), torch.zeros(2, 32, dtype=torch.uint8), torch.zeros(
+        2, 4, dtype=torch.uint8)
+    with pytest.raises(ValueError, match="GPU tensor"):
+        dsl.lora_mx4_quantize(x, q, s)
+    with pytest.raises(TypeError):
+        dsl.lora_mx4_quantize(x.float(), q, s)
+    with pytest.raises(TypeError):
+        dsl.lora_sample(None, None, None)
+
+
 # ---------------------------------------------------------------------------
 # the reference's own pins (values worked out by hand)
 # ---------------------------------------------------------------------------
