@@ -343,8 +343,9 @@ constexpr float kBinsPerUnit = (kHist - 2) / kRange;
 
 struct Fast {
     unsigned long long hist[kWaves][kHist];
-    uint32_t key[kList];
-    uint32_t idx[kList];
+    unsigned long long list[kList];          // place() of an element, its weight, its sub-bin
+    uint32_t list_w[kList];
+    int16_t list_sub[kList];
     unsigned long long sub[kThreads];
     unsigned long long few[kFew];            // place() of an element
     uint32_t few_w[kFew];
@@ -352,7 +353,8 @@ struct Fast {
     uint64_t scan[2 * kWaves];
     float red[2 * kWaves];
     uint32_t n;
-    uint32_t lo, hi;
+    uint32_t few_n;
+    uint64_t last;
     uint64_t all, sum;
     int pick;
 };
@@ -713,8 +715,6 @@ __device__ bool sample_mass(const SampleParams& p, const Settings& c, const Row&
             s.hist[wave][i] = 0;
         if (threadIdx.x == 0) {
             s.n = 0;
-            s.lo = 0xFFFFFFFFu;
-            s.hi = 0;
         }
         G.each([&](float l, int) {
             const float z = exponent(r, l);
@@ -753,8 +753,18 @@ __device__ bool sample_mass(const SampleParams& p, const Settings& c, const Row&
                 to = min(pick, f + 1);
             }
         }
-        // bins below `from` are kept whole, bins above `to` not at all
+        // bins below `from` are kept whole, bins above `to` not at all; sub-bins of
+        // the one where top-p cuts
         const float first_place = (float)from, end_place = to >= kHist - 1 ? INFINITY : (float)(to + 1);
+        auto sub_bin = [&](float at) {       // exact, so monotonous; of other bins: outside
+            return at >= (float)pick && (at < (float)(pick + 1) || pick == kHist - 1)
+                       ? (int)fminf((at - (float)pick) * kThreads, (float)(kThreads - 1))
+                       : -1;
+        };
+        s.sub[threadIdx.x] = 0;
+        if (threadIdx.x < kWaves)
+            s.range[threadIdx.x] = 0;
+        __syncthreads();
         G.gather(
             &s.n,
             [&](float l) {                   // so is not -inf
@@ -763,60 +773,43 @@ __device__ bool sample_mass(const SampleParams& p, const Settings& c, const Row&
             },
             [&](uint32_t slot, float l, int i) {
                 if (slot < kList) {
-                    s.key[slot] = order_key(l);
-                    s.idx[slot] = (uint32_t)i;
+                    const float z = exponent(r, l);
+                    const uint32_t w = weight_of_exponent(z);
+                    const int sub = sub_bin(bin_place(z));
+                    s.list[slot] = place(order_key(l), i);
+                    s.list_w[slot] = w;
+                    s.list_sub[slot] = (int16_t)sub;
+                    if (sub >= 0)
+                        atomicAdd(&s.sub[sub], (unsigned long long)w);
                 }
             });
         __syncthreads();
         const int n = (int)s.n;
         if (n > kList)
             return false;
-        auto exponent_of = [&](uint32_t k) {
-            const uint32_t b = k ^ ((k >> 31) ? 0x80000000u : 0xFFFFFFFFu);
-            return exponent(r, __builtin_bit_cast(float, b));
-        };
-        auto weight_of = [&](uint32_t k) { return weight_of_exponent(exponent_of(k)); };
         if (c.top_p < 1.0f && pick <= to) {
-            // where in its bin: sub-bins over the bin's keys
-            for (int i = threadIdx.x; i < n; i += kThreads) {
-                if (bin_of(bin_place(exponent_of(s.key[i]))) == pick) {
-                    atomicMin(&s.lo, s.key[i]);
-                    atomicMax(&s.hi, s.key[i]);
-                }
-            }
-            s.sub[threadIdx.x] = 0;
-            __syncthreads();
-            const uint32_t lo = s.lo, hi = s.hi;
-            const int shift = max(0, 22 - (int)__clz((int)(hi - lo)));     // (hi - lo) >> shift < 1024
-            for (int i = threadIdx.x; i < n; i += kThreads) {
-                const uint32_t k = s.key[i];
-                if (k >= lo && k <= hi)
-                    atomicAdd(&s.sub[(hi - k) >> shift], (unsigned long long)weight_of(k));
-            }
-            __syncthreads();
-            if (threadIdx.x == 0)
-                s.n = 0;
             const uint64_t o = s.sub[threadIdx.x];
             const uint64_t up = block_scan(o, s.scan) + pick_before;
             if (up >= mass && up - o < mass) {
                 s.pick = threadIdx.x;
                 s.sum = up - o;
             }
+            if (threadIdx.x == 0)
+                s.few_n = 0;
             __syncthreads();
             const int sub = s.pick;
             const uint64_t sub_before = s.sum;
-            for (int i = threadIdx.x; i < n; i += kThreads) {
-                const uint32_t k = s.key[i];
-                if (k >= lo && k <= hi && (int)((hi - k) >> shift) == sub) {
-                    const uint32_t at = atomicAdd(&s.n, 1u);
+#pragma unroll 1
+            for (int i = threadIdx.x; i < n; i += kThreads)
+                if (s.list_sub[i] == sub) {
+                    const uint32_t at = atomicAdd(&s.few_n, 1u);
                     if (at < kFew) {
-                        s.few[at] = place(k, (int)s.idx[i]);
-                        s.few_w[at] = weight_of(k);
+                        s.few[at] = s.list[i];
+                        s.few_w[at] = s.list_w[i];
                     }
                 }
-            }
             __syncthreads();
-            const int m = (int)s.n;
+            const int m = (int)s.few_n;
             if (m > kFew)
                 return false;
             const int share = few_share(m), me = threadIdx.x / share;
@@ -827,25 +820,22 @@ __device__ bool sample_mass(const SampleParams& p, const Settings& c, const Row&
             before = share_sum(before, share, s.scan) + sub_before;
             // the last one kept: its predecessors stay below the mass, with it they reach it
             if (me < m && threadIdx.x % share == 0 && before < mass && before + s.few_w[me] >= mass)
-                s.sub[0] = mine_at;
+                s.last = mine_at;
             __syncthreads();
-            last = s.sub[0];
+            last = s.last;
         }
         // kept weight of each range of indices
-        if (threadIdx.x < kWaves)
-            s.range[threadIdx.x] = 0;
-        __syncthreads();
-        {
-            uint64_t sum = 0;
-            for (int i = lane; i < from; i += 64)
-                sum += s.hist[wave][i];
-            if (sum)
-                atomicAdd(&s.range[wave], (unsigned long long)sum);
-        }
+        uint64_t sum = 0;
+        for (int i = lane; i < from; i += 64)
+            sum += s.hist[wave][i];
+        if (sum)
+            atomicAdd(&s.range[wave], (unsigned long long)sum);
+#pragma unroll 1
         for (int i = threadIdx.x; i < n; i += kThreads) {
-            const uint32_t k = s.key[i], w = weight_of(k);
-            if (w >= c.floor_w && place(k, (int)s.idx[i]) >= last)
-                atomicAdd(&s.range[((int)s.idx[i] + G.off) / kVec / G.run], (unsigned long long)w);
+            const uint64_t at = s.list[i];
+            const uint32_t w = s.list_w[i];
+            if (w >= c.floor_w && at >= last)
+                atomicAdd(&s.range[((int)place_column(at) + G.off) / kVec / G.run], (unsigned long long)w);
         }
         __syncthreads();
     }
