@@ -12,6 +12,9 @@ namespace {
 constexpr int64_t kMaxDim = (int64_t{1} << 31) - 1;
 constexpr int64_t kMaxGrid = (int64_t{1} << 31) - 1;
 constexpr int64_t kMaxGridY = 65535;
+constexpr int64_t kMaxColumns = int64_t{1} << 25;      // of a product
+constexpr int64_t kMaxTiles = int64_t{1} << 22;        // 64 x 128 tiles of a product's y
+constexpr int64_t kMaxDraws = int64_t{1} << 21;        // rows of one sampling call
 constexpr int64_t kMaxPitch = int64_t{1} << 23;        // bytes; 256 rows stay below 2^32
 constexpr int64_t kMaxVocabulary = int64_t{1} << 22;   // a row's weight stays below 2^53
 
@@ -81,7 +84,8 @@ int check_linear_sizes(int64_t M, int64_t K, int64_t N, int32_t split_k)
         return LORA_ERR_UNSUPPORTED;
     if (K % (kMxBlock * (int64_t)split_k) || N % 8)
         return LORA_ERR_UNSUPPORTED;
-    if ((M + 63) / 64 > kMaxGridY)
+    // what a launch holds: fewer than 2^32 threads
+    if ((M + 63) / 64 > kMaxGridY || N > kMaxColumns || ((M + 63) / 64) * ((N + 127) / 128) > kMaxTiles)
         return LORA_ERR_SHAPE;
     return LORA_OK;
 }
@@ -244,7 +248,7 @@ int lora_sample(const void* logits, int32_t logits_type, int64_t ld, int64_t B, 
                 const int32_t* top_k, const float* top_p, const float* min_p, const float* u, int32_t* tokens,
                 float* logprobs, void* stream)
 {
-    if (B < 0 || B > kMaxDim || V < 1)
+    if (B < 0 || B > kMaxDraws || V < 1)
         return LORA_ERR_SHAPE;
     if (V > kMaxVocabulary || (logits_type != LORA_LOGITS_BF16 && logits_type != LORA_LOGITS_F32))
         return LORA_ERR_UNSUPPORTED;

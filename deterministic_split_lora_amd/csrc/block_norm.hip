@@ -117,10 +117,8 @@ __device__ __forceinline__ void normalise(float (&v)[VPT][8], const NormParams& 
 }
 
 template <int VPT, int WAVES>
-__global__ void __launch_bounds__(WAVES * 64) k_block_norm(NormParams p)
+__device__ __forceinline__ void norm_row(const NormParams& p, int64_t row, float* buf)
 {
-    __shared__ float buf[4 * WAVES];
-    const int64_t row = blockIdx.x;
     float v[VPT][8];
     u32x4 rr[VPT];
 #pragma unroll
@@ -163,11 +161,26 @@ __global__ void __launch_bounds__(WAVES * 64) k_block_norm(NormParams p)
     }
 }
 
+// A launch holds fewer than 2^32 threads: beyond kMaxRows a workgroup takes
+// further rows.
+constexpr int64_t kMaxRows = int64_t{1} << 20;
+
+template <int VPT, int WAVES>
+__global__ void __launch_bounds__(WAVES * 64) k_block_norm(NormParams p)
+{
+    __shared__ float buf[4 * WAVES];
+    norm_row<VPT, WAVES>(p, blockIdx.x, buf);
+    for (int64_t row = (int64_t)blockIdx.x + kMaxRows; row < p.M; row += kMaxRows) {
+        __syncthreads();                     // the row before's sums have been read
+        norm_row<VPT, WAVES>(p, row, buf);
+    }
+}
+
 }  // namespace
 
 hipError_t launch_block_norm(const NormParams& p, hipStream_t st)
 {
-    const dim3 grid((unsigned)p.M);
+    const dim3 grid((unsigned)(p.M < kMaxRows ? p.M : kMaxRows));
     if (p.C <= 512)
         hipLaunchKernelGGL((k_block_norm<1, 1>), grid, dim3(64), 0, st, p);
     else if (p.C <= 2048)

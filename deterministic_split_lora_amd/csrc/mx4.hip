@@ -25,6 +25,7 @@ constexpr int kPass = kWave * kLaneElems;    // elements of one wave pass
 constexpr int kPasses = 4;
 constexpr int kSegment = kPass * kPasses;
 constexpr int kQuantWaves = 4;
+constexpr int64_t kMaxBlocks = int64_t{1} << 20;
 
 __device__ __forceinline__ uint32_t max_u16x2(uint32_t a, uint32_t b)
 {
@@ -33,22 +34,20 @@ __device__ __forceinline__ uint32_t max_u16x2(uint32_t a, uint32_t b)
                                                                   __builtin_bit_cast(u16x2, b)));
 }
 
-// Which row and which part of it this wave has; false past the last one.
-__device__ __forceinline__ bool wave_segment(const Mx4QuantParams& p, int64_t* row, int* k0)
+// f(row, this lane's first element) for each part of a row that this wave has.
+template <class F>
+__device__ __forceinline__ void wave_segments(const Mx4QuantParams& p, F f)
 {
     const uint32_t segs = ((uint32_t)p.K + kSegment - 1) / kSegment;
-    const int64_t item = (int64_t)blockIdx.x * kQuantWaves + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-    *row = item / segs;
-    *k0 = (int)(item - *row * segs) * kSegment + (threadIdx.x & 63) * kLaneElems;
-    return *row < p.M;
+    int64_t item = (int64_t)blockIdx.x * kQuantWaves + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    for (; item < p.M * segs; item += (int64_t)gridDim.x * kQuantWaves) {
+        const int64_t row = item / segs;
+        f(row, (int)(item - row * segs) * kSegment + (int)(threadIdx.x & 63) * kLaneElems);
+    }
 }
 
-__global__ void __launch_bounds__(kQuantWaves * kWave) k_mx4_quantize(Mx4QuantParams p)
+__device__ __forceinline__ void quantize_segment(const Mx4QuantParams& p, int64_t row, int k0)
 {
-    int64_t row;
-    int k0;
-    if (!wave_segment(p, &row, &k0))
-        return;
     u32x4 v[kPasses];
     const uint16_t* xr = p.x + row * p.ld_x;
 #pragma unroll
@@ -77,12 +76,8 @@ __global__ void __launch_bounds__(kQuantWaves * kWave) k_mx4_quantize(Mx4QuantPa
     }
 }
 
-__global__ void __launch_bounds__(kQuantWaves * kWave) k_mx4_dequantize(Mx4QuantParams p)
+__device__ __forceinline__ void dequantize_segment(const Mx4QuantParams& p, int64_t row, int k0)
 {
-    int64_t row;
-    int k0;
-    if (!wave_segment(p, &row, &k0))
-        return;
     uint32_t w[kPasses], b[kPasses];
 #pragma unroll
     for (int i = 0; i < kPasses; ++i) {
@@ -99,10 +94,22 @@ __global__ void __launch_bounds__(kQuantWaves * kWave) k_mx4_dequantize(Mx4Quant
     }
 }
 
+__global__ void __launch_bounds__(kQuantWaves * kWave) k_mx4_quantize(Mx4QuantParams p)
+{
+    wave_segments(p, [&](int64_t row, int k0) { quantize_segment(p, row, k0); });
+}
+
+__global__ void __launch_bounds__(kQuantWaves * kWave) k_mx4_dequantize(Mx4QuantParams p)
+{
+    wave_segments(p, [&](int64_t row, int k0) { dequantize_segment(p, row, k0); });
+}
+
+// A launch holds fewer than 2^32 threads; waves take further parts beyond that.
 unsigned quant_grid(const Mx4QuantParams& p)
 {
     const int64_t segs = ((int64_t)p.K + kSegment - 1) / kSegment;
-    return (unsigned)((p.M * segs + kQuantWaves - 1) / kQuantWaves);
+    const int64_t blocks = (p.M * segs + kQuantWaves - 1) / kQuantWaves;
+    return (unsigned)(blocks < kMaxBlocks ? blocks : kMaxBlocks);
 }
 
 }  // namespace

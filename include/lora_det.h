@@ -548,7 +548,8 @@ int lora_mx4_dequantize(const uint8_t* q, int64_t ld_q, const uint8_t* scales, i
  *   lora_mx4_linear_q  x as MX4 codes and scales [M] rows
  *   wq, ws             W as MX4 codes and scales, N rows
  *   y                  bf16 [M][ld_y], written; 16-byte aligned, ld_y % 8 == 0
- * split_k in {1, 2, 4, 8, 16}, K % (32 split_k) == 0, N % 8 == 0.
+ * split_k in {1, 2, 4, 8, 16}, K % (32 split_k) == 0, N % 8 == 0;
+ * M <= 64 * 65535, N <= 2^25, at most 2^22 tiles of 64 x 128 in y.
  * workspace: >= lora_mx4_linear_workspace_bytes(M, K, N, split_k) bytes,
  * 16-byte aligned, no initialisation needed (may be NULL when that is 0; 0 is
  * also returned for invalid input).
@@ -611,7 +612,8 @@ int lora_block_norm(const uint16_t* y, int64_t ld_y, int32_t post, const uint16_
  * logits: [B][ld] bf16 (LORA_LOGITS_BF16) or fp32 (LORA_LOGITS_F32), aligned to
  * their size, any ld >= V.  temperature, top_p, min_p, u: fp32 [B]; top_k: int32
  * [B]; temperature NULL: 1, top_k, top_p, min_p NULL: off.  u is required, in
- * [0, 1).  tokens: int32 [B].  logprobs: fp32 [B] or NULL.  1 <= V <= 2^22.
+ * [0, 1).  tokens: int32 [B].  logprobs: fp32 [B] or NULL.  1 <= V <= 2^22,
+ * B <= 2^21.
  */
 enum lora_logits_type { LORA_LOGITS_BF16 = 0, LORA_LOGITS_F32 = 1 };
 

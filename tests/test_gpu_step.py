@@ -113,6 +113,35 @@ def test_dequantize_every_scale():
     assert np.array_equal(f64(out), want, equal_nan=True)
 
 
+def test_more_rows_than_one_launch_holds():
+    """Past 2^20 workgroups a wave (a workgroup of the norm) takes further rows."""
+    t = torch()
+    M, K = (1 << 22) + 4099, 32
+    few = normal_bf16((4099, K), 1.0, 3, "x")
+    x = bf16_to_gpu(few).repeat(M // 4099 + 1, 1)[:M].contiguous()
+    q, s = t.empty(M, 16, dtype=t.uint8, device="cuda"), t.zeros(M, 4, dtype=t.uint8, device="cuda")
+    dsl.lora_mx4_quantize(x, q, s)
+    code, sc = step.mx4_quantize(bf16_to_f64(few))
+    want_q, want_s = u8_to_gpu(step.mx4_pack(code)), u8_to_gpu(sc)
+    out = t.empty_like(x)
+    dsl.lora_mx4_dequantize(q, s, out)
+    small = t.empty(4099, K, dtype=t.bfloat16, device="cuda")
+    dsl.lora_mx4_dequantize(q[:4099], s[:4099], small)
+    for a in range(0, M - 4099, 4099 * 97):
+        assert t.equal(q[a:a + 4099], want_q) and t.equal(s[a:a + 4099, :1], want_s)
+        assert t.equal(out[a:a + 4099].view(t.int16), small.view(t.int16))
+    tail = M // 4099 * 4099
+    assert t.equal(q[tail:], want_q[:M - tail]) and t.equal(out[tail:].view(t.int16), small[:M - tail].view(t.int16))
+    r, n = t.empty_like(x), t.empty_like(x)
+    dsl.lora_block_norm(x, r, y=out, post="rms", pre="layer", x_out=n)
+    r1, n1 = t.empty_like(small), t.empty_like(small)
+    dsl.lora_block_norm(x[:4099], r1, y=small, post="rms", pre="layer", x_out=n1)
+    for a in list(range(0, M - 4099, 4099 * 97)) + [tail]:
+        b = min(a + 4099, M)
+        assert t.equal(r[a:b].view(t.int16), r1[:b - a].view(t.int16))
+        assert t.equal(n[a:b].view(t.int16), n1[:b - a].view(t.int16))
+
+
 def test_conversions_of_no_rows():
     t = torch()
     x = t.empty(0, 64, dtype=t.bfloat16, device="cuda")

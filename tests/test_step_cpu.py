@@ -50,7 +50,10 @@ def linear(mx=False, **kw):
 
 LINEAR_REFUSALS = [
     (dict(M=-1), B.LORA_ERR_SHAPE), (dict(N=-8), B.LORA_ERR_SHAPE), (dict(K=0), B.LORA_ERR_SHAPE),
-    (dict(M=(1 << 31) - 1), B.LORA_ERR_SHAPE),
+    (dict(M=(1 << 31) - 1), B.LORA_ERR_SHAPE), (dict(N=(1 << 25) + 8, ld_y=1 << 26), B.LORA_ERR_SHAPE),
+    (dict(M=64 * 65535, N=1 << 14, ld_y=1 << 14), B.LORA_ERR_SHAPE),
+    (dict(ld_wq=(1 << 23) + 16), B.LORA_ERR_UNSUPPORTED), (dict(ld_ws=(1 << 23) + 4), B.LORA_ERR_UNSUPPORTED),
+    (dict(ld_x=(1 << 23) + 16), B.LORA_ERR_UNSUPPORTED),
     (dict(S=3), B.LORA_ERR_UNSUPPORTED), (dict(S=32), B.LORA_ERR_UNSUPPORTED), (dict(S=0), B.LORA_ERR_UNSUPPORTED),
     (dict(K=96, S=2), B.LORA_ERR_UNSUPPORTED), (dict(N=60), B.LORA_ERR_UNSUPPORTED),
     (dict(x=None), B.LORA_ERR_NULL), (dict(wq=None), B.LORA_ERR_NULL), (dict(ws=None), B.LORA_ERR_NULL),
@@ -123,7 +126,7 @@ def sample(**kw):
 
 
 @pytest.mark.parametrize("kw,status", [
-    (dict(B=-1), B.LORA_ERR_SHAPE), (dict(V=0), B.LORA_ERR_SHAPE), (dict(ld=99), B.LORA_ERR_SHAPE),
+    (dict(B=-1), B.LORA_ERR_SHAPE), (dict(B=(1 << 21) + 1), B.LORA_ERR_SHAPE), (dict(V=0), B.LORA_ERR_SHAPE), (dict(ld=99), B.LORA_ERR_SHAPE),
     (dict(V=(1 << 22) + 1, ld=1 << 23), B.LORA_ERR_UNSUPPORTED), (dict(type=2), B.LORA_ERR_UNSUPPORTED),
     (dict(logits=None), B.LORA_ERR_NULL), (dict(u=None), B.LORA_ERR_NULL), (dict(tok=None), B.LORA_ERR_NULL),
     (dict(logits=FAKE + 1), B.LORA_ERR_ALIGN), (dict(logits=MIS, type=1), B.LORA_ERR_ALIGN),
