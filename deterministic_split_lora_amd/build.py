@@ -16,7 +16,7 @@ LIB = os.path.join(HERE, "liblora_det.so")
 BINDING = os.path.join(HERE, "_native.so")
 SOURCES = ["abi.hip", "shrink.hip", "expand.hip", "fused.hip", "streamed.hip", "sgmv_plan.hip",
            "abi_step.hip", "mx4.hip", "mx4_linear.hip", "block_norm.hip", "sample.hip"]
-HEADERS = ["device.h", "kernels.h", "shrink_tile.h", "step_kernels.h", "mx4.h"]
+HEADERS = ["device.h", "kernels.h", "shrink_tile.h", "step_kernels.h", "mx4.h", "mx4_tile.h"]
 
 HIPCC_FLAGS = [
     "--offload-arch=gfx950",
