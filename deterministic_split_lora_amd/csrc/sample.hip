@@ -65,22 +65,89 @@ struct Acc {
     uint64_t w;                              // their weight
 };
 
+// Sums within a wave go through the vector unit's lane moves, a few cycles each;
+// a shuffle through LDS takes over a hundred, and a row alone on its CU waits for
+// every one (1 x 32000 top-k 15.0 -> 13.3 us).  Every lane of the wave has to be active.
+
+// v of the lane that the move CTRL reads, 0 where there is none.
+template <int CTRL, int ROWS = 0xF>
+__device__ __forceinline__ uint32_t moved(uint32_t v)
+{
+    return (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, CTRL, ROWS, 0xF, false);
+}
+
+template <int CTRL, int ROWS = 0xF>
+__device__ __forceinline__ uint64_t moved(uint64_t v)
+{
+    return (uint64_t)moved<CTRL, ROWS>((uint32_t)(v >> 32)) << 32 | moved<CTRL, ROWS>((uint32_t)v);
+}
+
+constexpr int kRowShift = 0x110;             // + d: the lane d below, in the same 16
+constexpr int kLane15 = 0x142, kLane31 = 0x143;   // last lane of the 16, 32 before
+constexpr int kXor1 = 0xB1, kXor2 = 0x4E;    // within four lanes
+constexpr int kMirror8 = 0x141, kMirror16 = 0x140;
+
+// Inclusive sum over the wave, in lane order.
+__device__ __forceinline__ uint64_t wave_scan(uint64_t v)
+{
+    v += moved<kRowShift + 1>(v);
+    v += moved<kRowShift + 2>(v);
+    v += moved<kRowShift + 4>(v);
+    v += moved<kRowShift + 8>(v);
+    v += moved<kLane15, 0xA>(v);             // to the second and fourth 16
+    v += moved<kLane31, 0xC>(v);             // to the upper 32
+    return v;
+}
+
+// op over each aligned group of `share` lanes (a power of two, at most 64, the
+// same in the whole wave); every lane gets it.  Where a mirror stands for a
+// distance of 4 or 8, the lanes it mixes up already hold the same value.
+template <class Op>
+__device__ __forceinline__ uint64_t wave_join(uint64_t v, int share, Op op)
+{
+    if (share > 1)
+        v = op(v, moved<kXor1>(v));
+    if (share > 2)
+        v = op(v, moved<kXor2>(v));
+    if (share > 4)
+        v = op(v, moved<kMirror8>(v));
+    if (share > 8)
+        v = op(v, moved<kMirror16>(v));
+    if (share > 16) {
+        const auto lo = __builtin_amdgcn_permlane16_swap((uint32_t)v, (uint32_t)v, false, false);
+        const auto hi = __builtin_amdgcn_permlane16_swap((uint32_t)(v >> 32), (uint32_t)(v >> 32), false, false);
+        v = op((uint64_t)hi[0] << 32 | lo[0], (uint64_t)hi[1] << 32 | lo[1]);
+    }
+    if (share > 32) {
+        const auto lo = __builtin_amdgcn_permlane32_swap((uint32_t)v, (uint32_t)v, false, false);
+        const auto hi = __builtin_amdgcn_permlane32_swap((uint32_t)(v >> 32), (uint32_t)(v >> 32), false, false);
+        v = op((uint64_t)hi[0] << 32 | lo[0], (uint64_t)hi[1] << 32 | lo[1]);
+    }
+    return v;
+}
+
+__device__ __forceinline__ uint64_t wave_sum(uint64_t v, int share = 64)
+{
+    return wave_join(v, share, [](uint64_t a, uint64_t b) { return a + b; });
+}
+
+__device__ __forceinline__ uint64_t wave_max(uint64_t v)
+{
+    return wave_join(v, 64, [](uint64_t a, uint64_t b) { return max(a, b); });
+}
+
 // Inclusive sum over the workgroup of one value a thread, in thread order.
 __device__ __forceinline__ uint64_t block_scan(uint64_t v, uint64_t* buf)
 {
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-#pragma unroll
-    for (int d = 1; d < 64; d <<= 1) {
-        const uint64_t u = __shfl_up((unsigned long long)v, d);
-        if (lane >= d)
-            v += u;
-    }
+    v = wave_scan(v);
     __syncthreads();
     if (lane == 63)
         buf[wave] = v;
     __syncthreads();
-    for (int i = 0; i < wave; ++i)
-        v += buf[i];
+#pragma unroll
+    for (int i = 0; i < kWaves - 1; ++i)
+        v += i < wave ? buf[i] : 0;
     return v;
 }
 
@@ -171,9 +238,7 @@ __device__ int locate(const Row& r, Shared& s, uint64_t t, F value)
         const int end = min(r.V, (g + 1) * seg_len);
         for (int i = g * seg_len + lane; i < end; i += 64)
             sum += value(i);
-#pragma unroll
-        for (int d = 1; d < 64; d <<= 1)
-            sum += __shfl_xor((unsigned long long)sum, d);
+        sum = wave_sum(sum);
         if (lane == 0)
             s.seg[g] = sum;
     }
@@ -194,12 +259,7 @@ __device__ int locate(const Row& r, Shared& s, uint64_t t, F value)
         for (int base = first; base < end; base += 64) {
             const int i = base + lane;
             uint64_t v = i < end ? value(i) : 0;
-#pragma unroll
-            for (int d = 1; d < 64; d <<= 1) {
-                const uint64_t u = __shfl_up((unsigned long long)v, d);
-                if (lane >= d)
-                    v += u;
-            }
+            v = wave_scan(v);
             const uint64_t hit = __ballot(run + v > t);
             if (hit) {
                 if (lane == 0)
@@ -550,9 +610,10 @@ __device__ __forceinline__ uint32_t place_column(uint64_t place)
 
 __device__ __forceinline__ float block_reduce_max(float v, float* buf)
 {
-#pragma unroll
-    for (int d = 1; d < 64; d <<= 1)
-        v = fmaxf(v, __shfl_xor(v, d));
+    v = __builtin_bit_cast(float, (uint32_t)wave_join(__builtin_bit_cast(uint32_t, v), 64, [](uint64_t a, uint64_t b) {
+        return (uint64_t)__builtin_bit_cast(
+            uint32_t, fmaxf(__builtin_bit_cast(float, (uint32_t)a), __builtin_bit_cast(float, (uint32_t)b)));
+    }));
     __syncthreads();
     if ((threadIdx.x & 63) == 0)
         buf[threadIdx.x >> 6] = v;
@@ -566,9 +627,7 @@ __device__ __forceinline__ float block_reduce_max(float v, float* buf)
 
 __device__ __forceinline__ uint64_t block_sum(uint64_t v, uint64_t* buf)
 {
-#pragma unroll
-    for (int d = 1; d < 64; d <<= 1)
-        v += __shfl_xor((unsigned long long)v, d);
+    v = wave_sum(v);
     __syncthreads();
     if ((threadIdx.x & 63) == 0)
         buf[threadIdx.x >> 6] = v;
@@ -601,8 +660,7 @@ __device__ __forceinline__ void over_few(int n, int share, F f)
 // Sum over the `share` neighbouring threads that stand for one element.
 __device__ __forceinline__ uint64_t share_sum(uint64_t v, int share, uint64_t* wide)
 {
-    for (int d = 1; d < min(share, 64); d <<= 1)
-        v += __shfl_xor((unsigned long long)v, d);
+    v = wave_sum(v, min(share, 64));
     if (share > 64) {                        // uniform: few elements, several waves each
         __syncthreads();
         if ((threadIdx.x & 63) == 0)
@@ -708,9 +766,7 @@ __device__ bool sample_mass(const SampleParams& p, const Settings& c, const Row&
     if (!cut) {
         uint64_t sum = 0;
         G.each([&](float l, int) { sum += weight_finite(r, l); });
-#pragma unroll
-        for (int d = 1; d < 64; d <<= 1)
-            sum += __shfl_xor((unsigned long long)sum, d);
+        sum = wave_sum(sum);
         if (lane == 0)
             s.range[wave] = sum;
         __syncthreads();
@@ -917,9 +973,7 @@ __global__ void __launch_bounds__(kThreads) k_sample(SampleParams p)
             best = fmaxf(best, l);
         });
         uint64_t top = best == -INFINITY ? 0 : place(order_key(best), at);
-#pragma unroll
-        for (int d = 1; d < 64; d <<= 1)
-            top = max(top, (uint64_t)__shfl_xor((unsigned long long)top, d));
+        top = wave_max(top);
         if ((threadIdx.x & 63) == 0)
             s.scan[threadIdx.x >> 6] = top;
         __syncthreads();
