@@ -17,6 +17,8 @@
 #include "device.h"
 #include "step_kernels.h"
 
+#include <float.h>
+
 namespace lora {
 
 namespace {
@@ -682,11 +684,12 @@ template <bool BF16>
 __device__ bool sample_top_k(const SampleParams& p, const Settings& c, const Row& r, const Groups<BF16>& G, Fast& s,
                              int64_t row, float mine)
 {
-    // bins over the maxima's range; a thread without logits has none
+    // bins over the maxima's range; a thread without logits has none.  `per` stays
+    // finite for any range, so that the maximum's own place is 0
     const float lowest = -block_reduce_max(mine == -INFINITY ? -INFINITY : -mine, s.red);
     if (!(r.lmax - lowest < INFINITY))
         return false;
-    const float per = lowest < r.lmax ? (kThreads - 1) / (r.lmax - lowest) : 0.0f;
+    float per = lowest < r.lmax ? fminf((kThreads - 1) / (r.lmax - lowest), FLT_MAX) : 0.0f;
     auto at = [&](float l) { return (r.lmax - l) * per; };
     uint32_t* count = reinterpret_cast<uint32_t*>(s.sub);
     count[threadIdx.x] = 0;
@@ -704,11 +707,15 @@ __device__ bool sample_top_k(const SampleParams& p, const Settings& c, const Row
     if (enough)
         s.pick = threadIdx.x;
     __syncthreads();
-    // with fewer than k maxima the k-th logit may lie below all of them
-    const bool all = block_sum(own, s.scan) < (uint64_t)c.k;
-    const float end_place = all ? INFINITY : (float)(s.pick + 1);
+    // with fewer than k maxima the k-th logit may lie below all of them, as far as
+    // the type reaches: every logit's place is 0
+    float end_place = (float)(s.pick + 1);
+    if (block_sum(own, s.scan) < (uint64_t)c.k) {
+        per = 0.0f;
+        end_place = 1.0f;
+    }
     G.gather(
-        &s.n, [&](float l) { return at(l) < end_place; },      // so is not -inf
+        &s.n, [&](float l) { return at(l) < end_place; },      // so is not -inf (NaN or infinite place)
         [&](uint32_t slot, float l, int i) {
             if (slot < kFew) {
                 s.few[slot] = place(order_key(l), i);
