@@ -56,7 +56,10 @@ __device__ __forceinline__ uint32_t weight(const Row& r, float l)
 {
     if (l == r.lmax)
         return 1u << 31;
-    const float z = (l - r.lmax) * r.inv_t;
+    // a difference past the largest float: of halves, whose product is then doubled
+    // (exact, both being powers of two; the temperature is past 2^100 if it counts)
+    const float d = l - r.lmax;
+    const float z = d == -INFINITY ? (0.5f * l - 0.5f * r.lmax) * r.inv_t * 2.0f : d * r.inv_t;
     // a masked logit, or one whose exponent is not a number (infinite maximum at
     // an infinite temperature), has no weight
     return l == -INFINITY || !(z == z) ? 0u : __float2uint_rn(expf(z) * kOne);
@@ -306,7 +309,7 @@ __device__ __forceinline__ void answer(const SampleParams& p, int64_t row, int t
 
 // Any row, by passes over it: the way for what the paths below do not take
 // (more ties than their lists hold, top-k above kThreads, infinite maxima or
-// inverse temperatures).
+// inverse temperatures, temperatures of 1e37 and more).
 __device__ void sample_any(const SampleParams& p, const Settings& c, const Row& r, Shared& s, int64_t row)
 {
     // the kept prefix: keys above `key`, and of those equal to it the first `quota`
@@ -1005,7 +1008,9 @@ __global__ void __launch_bounds__(kThreads) k_sample(SampleParams p)
         }
         return;
     }
-    const bool finite = r.lmax < INFINITY && r.inv_t > 0.0f && r.inv_t < INFINITY;
+    // also that a difference of logits past the largest float weighs nothing: from
+    // 1 / T = 22.2 / 3.4e38 on
+    const bool finite = r.lmax < INFINITY && r.inv_t > 1e-37f && r.inv_t < INFINITY;
     bool done = false;
     if (finite && c.k > 0 && c.k <= kThreads)
         done = sample_top_k<BF16>(p, c, r, G, s, row, mine);

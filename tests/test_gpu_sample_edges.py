@@ -63,3 +63,23 @@ def test_top_k_of_few_logits_far_apart(bf16):
     picks = np.flatnonzero(kept).tolist()
     assert len(picks) == 10
     rows_against_reference(l, bf16, [(1e12, 10, 1.0, 0.0)] * 12, (picks + picks)[:12], pad=0)
+
+
+@pytest.mark.parametrize("bf16", [False, True])
+def test_differences_beyond_the_largest_float(bf16):
+    """Logits of either sign near the type's ends at temperatures near them too: every token is drawn once by its share,
+    with and without cuts."""
+    l = np.array([3e38, -3e38, 1e38, 0.0, -1e38, -2e38, 2.5e38, -3.3e38])
+    V = l.size
+    rows, settings, picks = [], [], []
+    for T, k, p, m in [(3e38, 0, 1.0, 0.0), (1e38, 0, 1.0, 0.0), (2e37, 0, 1.0, 0.0), (3e38, 7, 1.0, 0.0),
+                       (3e38, 0, 0.95, 0.0), (1e38, 5, 1.0, 0.0), (3e38, 0, 1.0, 0.15), (3e38, 7, 0.92, 0.0)]:
+        # the logits as the type holds them
+        _, val = gpu_logits(l[None], bf16)
+        kept = step.kept_weights(val[0], np.float32(T), k, np.float32(p), np.float32(m))
+        for i in np.flatnonzero(kept > kept.sum() * 2.0 ** -18):
+            rows.append(l)
+            settings.append((T, k, p, m))
+            picks.append(int(i))
+    assert settings.count((3e38, 0, 1.0, 0.0)) == V, "every token has a weight at this temperature"
+    rows_against_reference(np.stack(rows), bf16, settings, picks)
