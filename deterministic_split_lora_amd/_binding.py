@@ -78,6 +78,10 @@ def lib():
         if L.lora_abi_version() != ABI_VERSION:
             raise ImportError(f"{LIBRARY_PATH} has ABI version {L.lora_abi_version()}, the binding "
                               f"expects {ABI_VERSION}: rebuild it")
+        # entry points are added without a new version: an older library lacks them
+        missing = [name for name in EXPORTED if not hasattr(L, name)]
+        if missing:
+            raise ImportError(f"{LIBRARY_PATH} lacks {', '.join(missing)}: rebuild it")
         L.lora_status_str.restype = ctypes.c_char_p
         L.lora_status_str.argtypes = [ctypes.c_int]
         L.lora_shrink_plan.restype = ctypes.c_int

@@ -84,6 +84,8 @@
 extern "C" {
 #endif
 
+/* Changes when a declaration or a layout changes.  Functions are added without
+   a new version; a program that loads the library checks for those it needs. */
 #define LORA_DET_ABI_VERSION 6
 
 enum lora_status {
