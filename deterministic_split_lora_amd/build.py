@@ -76,11 +76,14 @@ def binding_command(out: str) -> list:
 def build(verbose: bool = False) -> str:
     """Compile every source; always recompiles (a cross-compile, no GPU needed).
     Each source is compiled to an object in parallel, then the objects are
-    linked into the shared library."""
+    linked into the shared library.  The compiled marshalling needs torch's
+    headers besides; if it fails, the library is put in place all the same and
+    the failure raised afterwards."""
     from concurrent.futures import ThreadPoolExecutor
     inc = ["-I", os.path.join(os.path.dirname(HERE), "include")]
     tag = "%d" % os.getpid()
     objs = [os.path.join(CSRC, os.path.splitext(s)[0] + ".o.tmp" + tag) for s in SOURCES]
+    lib, native = LIB + ".tmp" + tag, BINDING + ".tmp" + tag
     compile_flags = [f for f in HIPCC_FLAGS if f != "-shared"]
     noise = "'-packed-fp32-ops' is not a recognized feature"
 
@@ -92,29 +95,36 @@ def build(verbose: bool = False) -> str:
         # that warning is harmless and filtered here
         return res.returncode, "\n".join(l for l in res.stderr.splitlines() if noise not in l)
 
+    def run_binding():
+        try:
+            return run(binding_command(native))
+        except Exception as e:               # no torch, or one without headers
+            return 1, f"{type(e).__name__}: {e}"
+
     try:
         jobs = [[hipcc(), *compile_flags, *inc, "-c", os.path.join(CSRC, s), "-o", o]
                 for s, o in zip(SOURCES, objs)]
-        native = BINDING + ".tmp" + tag
-        objs.append(native)                  # removed below if it is not put in place
-        jobs.append(binding_command(native))
-        with ThreadPoolExecutor(max_workers=min(len(jobs), os.cpu_count() or 1)) as ex:
+        with ThreadPoolExecutor(max_workers=min(len(jobs) + 1, os.cpu_count() or 1)) as ex:
+            binding = ex.submit(run_binding)
             results = list(ex.map(run, jobs))
-        errs = "\n".join(e for _, e in results if e.strip())
+        binding_rc, binding_errs = binding.result()
+        errs = "\n".join(e for _, e in results + [(0, binding_errs)] if e.strip())
         if any(rc != 0 for rc, _ in results):
-            raise RuntimeError("compilation failed:\n" + errs)
+            raise RuntimeError("hipcc failed:\n" + errs)
         if verbose and errs:
             print(errs, file=sys.stderr)
-        objs.remove(native)
-        os.replace(native, BINDING)
-        tmp = LIB + ".tmp" + tag
-        rc, err = run([hipcc(), "--offload-arch=gfx950", "-shared", "-fPIC", *objs, "-o", tmp])
+        rc, err = run([hipcc(), "--offload-arch=gfx950", "-shared", "-fPIC", *objs, "-o", lib])
         if rc != 0:
             raise RuntimeError("hipcc link failed:\n" + err)
-        os.replace(tmp, LIB)
+        os.replace(lib, LIB)
         _record_revision()
+        if binding_rc != 0:
+            if os.path.exists(BINDING):      # an earlier one may not fit this library
+                os.remove(BINDING)
+            raise RuntimeError("the library is built, its compiled marshalling is not:\n" + binding_errs)
+        os.replace(native, BINDING)
     finally:
-        for o in objs:
+        for o in [*objs, lib, native]:
             if os.path.exists(o):
                 os.remove(o)
     return LIB

@@ -18,3 +18,27 @@ def test_library_without_the_newer_entry_points_is_refused(tmp_path, monkeypatch
     with pytest.raises(ImportError, match="lora_mx4_quantize.*lora_sample.*rebuild"):
         B.lib()
     assert B._lib is None
+
+
+def test_the_library_is_built_where_the_binding_does_not_compile(tmp_path, monkeypatch):
+    """The entry points that need no torch headers stay available, and the failure is still reported."""
+    from deterministic_split_lora_amd import build as b
+    lib, native = tmp_path / "liblora_det.so", tmp_path / "_native.so"
+    monkeypatch.setattr(b, "LIB", str(lib))
+    monkeypatch.setattr(b, "BINDING", str(native))
+    monkeypatch.setattr(b, "SOURCES", ["sgmv_plan.hip"])       # one is enough here, and seconds
+    monkeypatch.setattr(b, "_record_revision", lambda: None)
+    native.write_text("an earlier build's")
+    monkeypatch.setattr(b, "binding_command", lambda out: ["sh", "-c", "echo no such header >&2; exit 1"])
+    with pytest.raises(RuntimeError, match="no such header"):
+        b.build()
+    assert lib.exists() and not native.exists()
+    assert [p.name for p in tmp_path.iterdir()] == ["liblora_det.so"], "left temporary files"
+
+    def no_torch(out):
+        raise ImportError("no torch headers")
+    lib.unlink()
+    monkeypatch.setattr(b, "binding_command", no_torch)
+    with pytest.raises(RuntimeError, match="no torch headers"):
+        b.build()
+    assert lib.exists()
