@@ -570,8 +570,14 @@ def _native():
         if not os.path.exists(NATIVE_PATH):
             raise ImportError(f"{NATIVE_PATH} is missing: build it with `python -m deterministic_split_lora_amd.build`")
         spec = importlib.util.spec_from_file_location(__package__ + "._native", NATIVE_PATH)
-        m = importlib.util.module_from_spec(spec)
-        spec.loader.exec_module(m)
+        try:
+            m = importlib.util.module_from_spec(spec)
+            spec.loader.exec_module(m)
+        except ImportError as e:
+            raise ImportError(f"{NATIVE_PATH} does not load with torch {torch.__version__}, rebuild it: {e}") from e
+        built_for = getattr(m, "torch_version", "of an unknown version")
+        if built_for != torch.__version__:
+            raise ImportError(f"{NATIVE_PATH} is built for torch {built_for}, this is {torch.__version__}: rebuild it")
         L = lib()
         m.bind(*(ctypes.cast(getattr(L, name), _vp).value for name in (
             "lora_mx4_quantize", "lora_mx4_dequantize", "lora_mx4_linear", "lora_mx4_linear_q", "lora_block_norm",

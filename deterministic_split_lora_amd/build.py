@@ -68,7 +68,8 @@ def binding_command(out: str) -> list:
     from torch.utils import cpp_extension
     include = ["-isystem" + i for i in cpp_extension.include_paths()] + ["-I" + sysconfig.get_paths()["include"]]
     return ["g++", "-O2", "-std=c++17", "-fPIC", "-shared", "-fvisibility=hidden", "-Wall",
-            "-D_GLIBCXX_USE_CXX11_ABI=%d" % torch._C._GLIBCXX_USE_CXX11_ABI, *include,
+            "-D_GLIBCXX_USE_CXX11_ABI=%d" % torch._C._GLIBCXX_USE_CXX11_ABI,
+            '-DLORA_TORCH_VERSION="%s"' % torch.__version__, *include,
             os.path.join(CSRC, "binding.cpp"), "-o", out, "-L" + cpp_extension.library_paths()[0],
             "-ltorch_python", "-ltorch_cpu", "-lc10"]
 

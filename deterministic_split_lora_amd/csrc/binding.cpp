@@ -297,5 +297,11 @@ PyModuleDef module = {PyModuleDef_HEAD_INIT, "_native", nullptr, -1, methods, nu
 
 PyMODINIT_FUNC PyInit__native()
 {
-    return PyModule_Create(&module);
+    PyObject* m = PyModule_Create(&module);
+    // the torch whose objects' layout is compiled in; _binding.py compares it
+    if (m && PyModule_AddStringConstant(m, "torch_version", LORA_TORCH_VERSION) != 0) {
+        Py_DECREF(m);
+        return nullptr;
+    }
+    return m;
 }

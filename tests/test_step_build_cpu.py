@@ -42,3 +42,23 @@ def test_the_library_is_built_where_the_binding_does_not_compile(tmp_path, monke
     with pytest.raises(RuntimeError, match="no torch headers"):
         b.build()
     assert lib.exists()
+
+
+def test_binding_of_another_torch_is_refused(monkeypatch):
+    """The compiled marshalling reads torch's objects by the layout it was built for."""
+    import torch
+    B._native()
+    monkeypatch.setattr(B, "_native_module", None)
+    monkeypatch.setattr(torch, "__version__", "0.1+other")
+    with pytest.raises(ImportError, match="0.1.other.*rebuild"):
+        B._native()
+    assert B._native_module is None
+
+
+def test_binding_that_does_not_load_is_refused(tmp_path, monkeypatch):
+    broken = tmp_path / "_native.so"
+    broken.write_bytes(b"not a library")
+    monkeypatch.setattr(B, "_native_module", None)
+    monkeypatch.setattr(B, "NATIVE_PATH", str(broken))
+    with pytest.raises(ImportError, match="rebuild"):
+        B._native()
