@@ -44,23 +44,32 @@ typedef __attribute__((address_space(3))) uint8_t lds_u8;
 // Loads of 64 lanes straight to LDS, 16 (4) bytes a lane in lane order.  They
 // write no registers, so the compiler need not know when they land; the kernel
 // waits for them by count (wait_loads_and_meet).
+// They take the LDS address from m0, which the compiler reserves for its own use;
+// it is named as written all the same, so that no value of its is kept there over
+// them, and the compiler's remark on that is off.
+#pragma clang diagnostic push
+#pragma clang diagnostic ignored "-Winline-asm"
+
 // From `base` plus a lane's offset to LDS at `to` + AT.
 template <int AT>
 __device__ __forceinline__ void load_to_lds16(const uint8_t* base, uint32_t offset, uint32_t to)
 {
     asm volatile("s_add_u32 m0, %1, %3\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %0, %2" ::"v"(offset), "s"(to), "s"(base),
                  "n"(AT)
-                 : "memory", "scc");
+                 : "memory", "scc", "m0");
 }
 
 template <int BYTES>
 __device__ __forceinline__ void load_scales_to_lds(const uint8_t* from, uint32_t to)
 {
     if constexpr (BYTES == 16)
-        asm volatile("s_mov_b32 m0, %1\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %0, off" ::"v"(from), "s"(to) : "memory");
+        asm volatile("s_mov_b32 m0, %1\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %0, off" ::"v"(from), "s"(to)
+                     : "memory", "m0");
     else
-        asm volatile("s_mov_b32 m0, %1\n\ts_nop 0\n\tglobal_load_lds_dword %0, off" ::"v"(from), "s"(to) : "memory");
+        asm volatile("s_mov_b32 m0, %1\n\ts_nop 0\n\tglobal_load_lds_dword %0, off" ::"v"(from), "s"(to)
+                     : "memory", "m0");
 }
+#pragma clang diagnostic pop
 
 // Waits until at most N of this wave's loads are outstanding and its LDS reads
 // are done, then meets the workgroup.
