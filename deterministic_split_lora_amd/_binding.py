@@ -597,7 +597,7 @@ def _stream_address(stream, like):
 
 def lora_mx4_quantize(x, q, scales, stream=None):
     """q, scales = MX4 codes and block scales of x's rows (x [M,K] bf16, q [M,K/2] uint8, scales uint8 of M rows
-    with a row stride that is a multiple of 4)."""
+    with a row stride that is a multiple of 4; one of 16 lets the products read them faster)."""
     st = (_native_module or _native()).mx4_quantize(x, q, scales, _stream_address(stream, x))
     if st:
         raise LoraError(st, "lora_mx4_quantize")

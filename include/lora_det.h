@@ -512,9 +512,11 @@ int lora_sgmv_expand(const float* h, int64_t ld_h, const uint16_t* const* B_ptrs
  *           high four bits of byte i; 16-byte aligned, ld_q % 16 == 0,
  *           ld_q >= K / 2
  *   scales  uint8 [rows][ld_s bytes]: byte j for elements 32j .. 32j + 31;
- *           4-byte aligned, ld_s % 4 == 0, ld_s >= K / 32 (so every row's last
- *           aligned word can be read; bytes past K / 32 are ignored and left
- *           as they are)
+ *           4-byte aligned, ld_s % 4 == 0, ld_s >= K / 32.  Bytes past K / 32
+ *           are ignored and left as they are, but may be read: of every row, the
+ *           last one included, up to the next multiple of 4 bytes, and of 16
+ *           where the address and ld_s are multiples of 16 (the faster choice
+ *           for the products)
  * Leading dimensions of MX4 operands, and of a product's x, are at most 2^23
  * bytes.
  * ------------------------------------------------------------------------- */
