@@ -544,10 +544,12 @@ int lora_mx4_dequantize(const uint8_t* q, int64_t ld_q, const uint8_t* scales, i
  *     y[i][n] = bf16_rne( (..(C_0 + C_1) + ..) + C_{S-1} )
  *     C_s = sum over chunk s (K / split_k consecutive k) of x[i][k] W[n][k]
  * C_s is one chain of matrix-core steps in ascending k with an fp32
- * accumulator; the chunks are added in ascending order in fp32.  W enters with
- * its exact values.  A row's bits depend on x's row, W, K and split_k only,
- * whatever kernel M and N select.  split_k = 4..16 suits few rows (the chunks
- * run in parallel), 1 suits many (no sums to join).
+ * accumulator; the chunks are added in ascending order in fp32.  Operands enter
+ * with their exact values, except that with bf16 x a value of W past bf16's range
+ * is infinite, as from lora_mx4_dequantize (scale bytes 253 and 254, which
+ * lora_mx4_quantize never writes).  A row's bits depend on x's row, W, K and
+ * split_k only, whatever kernel M and N select.  split_k = 4..16 suits few rows
+ * (the chunks run in parallel), 1 suits many (no sums to join).
  *   lora_mx4_linear    x bf16 [M][ld_x], 16-byte aligned, ld_x % 8 == 0
  *   lora_mx4_linear_q  x as MX4 codes and scales [M] rows
  *   wq, ws             W as MX4 codes and scales, N rows

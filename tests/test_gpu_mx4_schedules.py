@@ -4,6 +4,7 @@ import numpy as np
 import pytest
 
 import deterministic_split_lora_amd as dsl
+from oracle import step
 from tests.helpers import bf16_from_gpu, gpu_available, torch
 from tests.test_gpu_step import Product, check_padding, f64, padded, quantized
 
@@ -121,3 +122,47 @@ def test_quantised_x_against_its_values_with_a_workspace():
         call(y, ws)
         t.cuda.synchronize()
         p.check(f64(y), S)
+
+
+@pytest.mark.parametrize("M", [3, 300])
+def test_largest_scales(M):
+    """With MX4 x, W's values enter exactly whatever their scale.  With bf16 x they do up to the scale byte 252, the largest
+    that quantisation writes; beyond it a value past bf16's range is infinite, as from lora_mx4_dequantize."""
+    t = torch()
+    K, N = 128, 136
+    codes = np.tile(np.arange(1, 8, dtype=np.uint8), K)[:K]
+    p = Product(M, K, N, 9, True)
+    p.wc = np.tile(codes, (N, 1))
+    p.wc[1::2] |= 8
+    p.wsc[:] = 252
+    p.wsc[10:12] = 253
+    p.wsc[20:22] = 254
+    p.wc[22:24] = 2                                            # 1.0: 2^127 is finite
+    p.wsc[22:24] = 254
+    p.w = step.mx4_values(p.wc, p.wsc)
+    p.xc = np.full((M, K), 3, dtype=np.uint8)                  # 1.5, positive: no sum cancels
+    p.xsc[:] = 100
+    p.x = step.mx4_values(p.xc, p.xsc)
+    p.gpu()
+    p.check(f64(product(p, 1)[0]), 1)
+
+    x, deq = t.empty(M, K, dtype=t.bfloat16, device="cuda"), t.empty(N, K, dtype=t.bfloat16, device="cuda")
+    dsl.lora_mx4_dequantize(p.xg, p.xs, x)
+    dsl.lora_mx4_dequantize(p.wq, p.ws, deq)
+    p.xg, p.mx = x, False
+    got = f64(product(p, 1)[0])
+    inf = np.isinf(f64(deq)).any(1)
+    assert np.flatnonzero(inf).tolist() == [10, 11, 20, 21]
+    assert np.array_equal(got[:, inf], np.tile(np.where(np.arange(N)[inf] % 2, -np.inf, np.inf), (M, 1)))
+    e = p.x @ p.w.T
+    tol = 2.0 ** -8 * np.abs(e) + (128 + 2) * 2.0 ** -23 * (np.abs(p.x) @ np.abs(p.w).T)
+    assert np.all(np.abs(got - e)[:, ~inf] <= tol[:, ~inf])
+
+
+def test_quantisation_writes_no_scale_past_252():
+    """Of every finite bf16 magnitude."""
+    t = torch()
+    v = np.arange(0x7F80, dtype=np.uint16)
+    x = t.from_numpy(np.repeat(v[:, None], 32, 1).view(np.int16)).cuda().view(t.bfloat16)
+    _, _, _, scales = quantized(x, v.size, 32)
+    assert scales.max() == 252
