@@ -20,6 +20,7 @@ namespace {
 
 constexpr int kStepK = 128;                  // k of one step's loads
 constexpr int kScaleSteps = 16;              // steps whose scales are loaded together
+constexpr int kRowsThreads = 1024;           // at most, of a workgroup of few rows: 16 chunks
 
 __device__ __forceinline__ MxOperand mx_operand(u32x4 q, uint32_t s, bool ok)
 {
@@ -38,7 +39,7 @@ __device__ __forceinline__ T load_at(const uint8_t* base, uint32_t offset)
     return *(global_t*)((global_u8*)base + offset);
 }
 
-// Few tokens: a workgroup owns 16 RT tokens x 16 CT columns (times the column
+// Few tokens: a workgroup owns 16 RT tokens x 16 columns (times the column
 // groups), its wave (group, s) the chain of chunk s; the chains meet in LDS.
 // Bound by how many loads are in flight: W's come D steps of 128 k ahead, those
 // of x (which the other workgroups read too, so that it is near) DX ahead, and a
@@ -49,8 +50,8 @@ __device__ __forceinline__ T load_at(const uint8_t* base, uint32_t offset)
 // bytes a row and step they would come from L2 every time, a line each.  Measured
 // on MI355X: 1 x 4096 x 6144 in 8 chunks 7.2 us, MX4 x 16 x 8192 x 8192 in 8
 // chunks 11.4 us (36 MB, 3.2 TB/s).
-template <bool XMX, int RT, int CT, int D, int DX, int THREADS>
-__global__ void __launch_bounds__(THREADS) k_mx4_linear_rows(Mx4LinearParams p, int groups)
+template <bool XMX, int RT, int D, int DX>
+__global__ void __launch_bounds__(kRowsThreads) k_mx4_linear_rows(Mx4LinearParams p, int groups)
 {
     static_assert(D % DX == 0 && kScaleSteps % D == 0, "the rings turn together");
     extern __shared__ float lds[];
@@ -59,15 +60,13 @@ __global__ void __launch_bounds__(THREADS) k_mx4_linear_rows(Mx4LinearParams p, 
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int S = p.split_k;
     const int chunk = wave % S, group = wave / S;             // wave = group * S + chunk
-    const int64_t n0 = ((int64_t)blockIdx.x * groups + group) * (16 * CT);
+    const int64_t n0 = ((int64_t)blockIdx.x * groups + group) * 16;
     const int64_t m0 = (int64_t)blockIdx.y * (16 * RT);
 
-    f32x4 acc[RT][CT];
+    f32x4 acc[RT];
 #pragma unroll
     for (int r = 0; r < RT; ++r)
-#pragma unroll
-        for (int c = 0; c < CT; ++c)
-            acc[r][c] = f32x4{0, 0, 0, 0};
+        acc[r] = f32x4{0, 0, 0, 0};
 
     const int64_t kc = (int64_t)chunk * p.k_chunk;
     const int steps = (p.k_chunk + kStepK - 1) / kStepK, last = steps - 1;
@@ -83,13 +82,9 @@ __global__ void __launch_bounds__(THREADS) k_mx4_linear_rows(Mx4LinearParams p, 
     const uint8_t* xs0 = XMX ? p.xs + m0 * p.ld_xs : nullptr;
     const int sb0 = (int)(kc / kMxBlock);                      // the chunk's first scale byte
     const int last_word = (p.k_chunk / kMxBlock * S - 1) >> 2;
-    uint32_t wo[CT], wso[CT], xo[RT], xso[RT];
-#pragma unroll
-    for (int c = 0; c < CT; ++c) {
-        const int64_t n = min(nb + 16 * c + li, p.N - 1) - nb;
-        wo[c] = (uint32_t)(n * p.ld_wq) + 16 * g;
-        wso[c] = (uint32_t)(n * p.ld_ws);
-    }
+    const int64_t n_li = min(nb + li, p.N - 1) - nb;
+    const uint32_t wo = (uint32_t)(n_li * p.ld_wq) + 16 * g, wso = (uint32_t)(n_li * p.ld_ws);
+    uint32_t xo[RT], xso[RT];
 #pragma unroll
     for (int r = 0; r < RT; ++r) {
         const int64_t m = min(m0 + 16 * r + li, p.M - 1) - m0;
@@ -97,12 +92,12 @@ __global__ void __launch_bounds__(THREADS) k_mx4_linear_rows(Mx4LinearParams p, 
         xso[r] = XMX ? (uint32_t)(m * p.ld_xs) : 0;
     }
 
-    u32x4 w[D][CT], x[DX][RT][XMX ? 1 : 4];
+    u32x4 w[D], x[DX][RT][XMX ? 1 : 4];
 
-    // This wave's scales, W's tiles first: [tile][16 rows][kScaleSteps words], a
+    // This wave's scales, W's tile first: [tile][16 rows][kScaleSteps words], a
     // word the four blocks of a step.
-    constexpr int kTile = 256, kScaleTiles = CT + (XMX ? RT : 0);
-    constexpr int kWaveLds = (RT * CT > kScaleTiles ? RT * CT : kScaleTiles) * kTile;
+    constexpr int kTile = 256, kScaleTiles = XMX ? 1 + RT : 1;
+    constexpr int kWaveLds = (RT > kScaleTiles ? RT : kScaleTiles) * kTile;
     uint32_t* sc = reinterpret_cast<uint32_t*>(lds) + wave * kWaveLds;
     const int shift = 8 * (sb0 & 3);
     // Loaded a run of steps ahead and put into LDS when the run begins: a load that
@@ -118,8 +113,8 @@ __global__ void __launch_bounds__(THREADS) k_mx4_linear_rows(Mx4LinearParams p, 
         const bool inside = word + 4 <= last_word;
 #pragma unroll
         for (int i = 0; i < kScaleTiles; ++i) {
-            const uint8_t* s0 = i < CT ? ws0 : xs0;
-            const uint32_t off = i < CT ? wso[i < CT ? i : 0] : xso[i < CT ? 0 : i - CT];
+            const uint8_t* s0 = i == 0 ? ws0 : xs0;
+            const uint32_t off = i == 0 ? wso : xso[i == 0 ? 0 : i - 1];
             if (inside) {
                 const u32x4 q = load_at<u32x4_word_aligned>(s0, off + 4 * word);
 #pragma unroll
@@ -143,12 +138,7 @@ __global__ void __launch_bounds__(THREADS) k_mx4_linear_rows(Mx4LinearParams p, 
             *reinterpret_cast<u32x4*>(sc + i * kTile + li * kScaleSteps + 4 * g) = q;
         }
     };
-    auto load_w = [&](u32x4 (&b)[CT], int j) {
-        const uint32_t less = j == last ? back : 0;
-#pragma unroll
-        for (int c = 0; c < CT; ++c)
-            b[c] = load_at<u32x4>(wq0 + j * 64, wo[c] - less);
-    };
+    auto load_w = [&](u32x4& b, int j) { b = load_at<u32x4>(wq0 + j * 64, wo - (j == last ? back : 0)); };
     auto load_x = [&](u32x4 (&b)[RT][XMX ? 1 : 4], int j) {
         const uint32_t less = j == last ? back : 0;
 #pragma unroll
@@ -163,38 +153,24 @@ __global__ void __launch_bounds__(THREADS) k_mx4_linear_rows(Mx4LinearParams p, 
         }
     };
     auto scales = [&](int tile, int j) { return sc[tile * kTile + li * kScaleSteps + j % kScaleSteps]; };
-    auto multiply = [&](u32x4 (&a)[CT], u32x4 (&b)[RT][XMX ? 1 : 4], int j) {
+    auto multiply = [&](u32x4& a, u32x4 (&b)[RT][XMX ? 1 : 4], int j) {
         if constexpr (XMX) {
             const bool ok = j < last || g < rem;
-            MxOperand wm[CT];
+            const MxOperand wm = mx_operand(a, scales(0, j) >> (8 * g), ok);
 #pragma unroll
-            for (int c = 0; c < CT; ++c)
-                wm[c] = mx_operand(a[c], scales(c, j) >> (8 * g), ok);
-#pragma unroll
-            for (int r = 0; r < RT; ++r) {
-                const MxOperand xm = mx_operand(b[r][0], scales(CT + r, j) >> (8 * g), ok);
-#pragma unroll
-                for (int c = 0; c < CT; ++c)
-                    acc[r][c] = mfma_mx4(wm[c], xm, acc[r][c]);
-            }
+            for (int r = 0; r < RT; ++r)
+                acc[r] = mfma_mx4(wm, mx_operand(b[r][0], scales(1 + r, j) >> (8 * g), ok), acc[r]);
         } else {
-            uint32_t s4[CT];
-#pragma unroll
-            for (int c = 0; c < CT; ++c) {
-                transpose_groups(a[c]);
-                s4[c] = scales(c, j);
-            }
+            transpose_groups(a);
+            const uint32_t s4 = scales(0, j);
 #pragma unroll
             for (int s = 0; s < 4; ++s) {
                 if (j == last && s >= rem)
                     break;
+                const bf16x8 wb = mx4_to_bf16(a[s], mx_scale_f32((s4 >> (8 * s)) & 255u));
 #pragma unroll
-                for (int c = 0; c < CT; ++c) {
-                    const bf16x8 wb = mx4_to_bf16(a[c][s], mx_scale_f32((s4[c] >> (8 * s)) & 255u));
-#pragma unroll
-                    for (int r = 0; r < RT; ++r)
-                        acc[r][c] = mfma_16x16x32(wb, __builtin_bit_cast(bf16x8, b[r][s]), acc[r][c]);
-                }
+                for (int r = 0; r < RT; ++r)
+                    acc[r] = mfma_16x16x32(wb, __builtin_bit_cast(bf16x8, b[r][s]), acc[r]);
             }
         }
     };
@@ -231,18 +207,16 @@ __global__ void __launch_bounds__(THREADS) k_mx4_linear_rows(Mx4LinearParams p, 
             load_x(x[d % DX], min(j + DX + d, last));
     }
 
-    // chains to LDS: [group][chunk][r][c][lane][4], then a thread adds its
+    // chains to LDS: [group][chunk][r][lane][4], then a thread adds its
     // output's chunks in ascending order
     float* mine = lds + wave * kWaveLds;     // wave = group * S + chunk
 #pragma unroll
     for (int r = 0; r < RT; ++r)
-#pragma unroll
-        for (int c = 0; c < CT; ++c)
-            *reinterpret_cast<f32x4*>(mine + (r * CT + c) * kTile + lane * 4) = acc[r][c];
+        *reinterpret_cast<f32x4*>(mine + r * kTile + lane * 4) = acc[r];
     __syncthreads();
-    const int quads = groups * RT * CT * 64;
+    const int quads = groups * RT * 64;
     for (int i = threadIdx.x; i < quads; i += blockDim.x) {
-        const int l = i & 63, tile = (i >> 6) % (RT * CT), grp = (i >> 6) / (RT * CT);
+        const int l = i & 63, tile = (i >> 6) % RT, grp = (i >> 6) / RT;
         const float* src = lds + grp * S * kWaveLds + tile * kTile + l * 4;
         f32x4 sum = *reinterpret_cast<const f32x4*>(src);
         for (int s = 1; s < S; ++s) {
@@ -251,8 +225,8 @@ __global__ void __launch_bounds__(THREADS) k_mx4_linear_rows(Mx4LinearParams p, 
             for (int e = 0; e < 4; ++e)
                 sum[e] += v[e];
         }
-        const int64_t m = m0 + 16 * (tile / CT) + (l & 15);
-        const int64_t n = ((int64_t)blockIdx.x * groups + grp) * (16 * CT) + 16 * (tile % CT) + 4 * (l >> 4);
+        const int64_t m = m0 + 16 * tile + (l & 15);
+        const int64_t n = ((int64_t)blockIdx.x * groups + grp) * 16 + 4 * (l >> 4);
         if (m < p.M && n < p.N) {
             const uint32_t lo = f32_to_bf16_bits(sum[0]) | (uint32_t)f32_to_bf16_bits(sum[1]) << 16;
             const uint32_t hi = f32_to_bf16_bits(sum[2]) | (uint32_t)f32_to_bf16_bits(sum[3]) << 16;
@@ -261,16 +235,15 @@ __global__ void __launch_bounds__(THREADS) k_mx4_linear_rows(Mx4LinearParams p, 
     }
 }
 
-template <bool XMX, int RT, int CT, int D, int DX, int THREADS>
+template <bool XMX, int RT, int D, int DX>
 hipError_t launch_rows(const Mx4LinearParams& p, hipStream_t st)
 {
     const int groups = p.split_k < 4 ? 4 / p.split_k : 1;
-    const int64_t cols = 16 * CT * groups;
+    const int64_t cols = 16 * groups;
     const dim3 grid((unsigned)((p.N + cols - 1) / cols), (unsigned)((p.M + 16 * RT - 1) / (16 * RT)));
-    const int tiles = RT * CT > CT + (XMX ? RT : 0) ? RT * CT : CT + (XMX ? RT : 0);
+    const int tiles = XMX ? 1 + RT : RT;
     const size_t lds = (size_t)groups * p.split_k * tiles * 1024;
-    hipLaunchKernelGGL((k_mx4_linear_rows<XMX, RT, CT, D, DX, THREADS>), grid, dim3(64 * groups * p.split_k), lds, st,
-                       p, groups);
+    hipLaunchKernelGGL((k_mx4_linear_rows<XMX, RT, D, DX>), grid, dim3(64 * groups * p.split_k), lds, st, p, groups);
     return hipGetLastError();
 }
 
@@ -397,19 +370,19 @@ hipError_t launch_mx4_linear(const Mx4LinearParams& p, bool x_is_mx4, hipStream_
         // eight steps ahead where a chain has more than four: 16 x 8192 x 8192 in 8
         // chunks 11.9 us against 15.1; in 16 chunks of four steps 13.7 against 19.4
         if (p.M <= 16)
-            return p.k_chunk > 4 * kStepK ? launch_rows<true, 1, 1, 8, 4, 1024>(p, st)
-                                          : launch_rows<true, 1, 1, 4, 4, 1024>(p, st);
+            return p.k_chunk > 4 * kStepK ? launch_rows<true, 1, 8, 4>(p, st)
+                                          : launch_rows<true, 1, 4, 4>(p, st);
         if (p.M <= 32)
-            return launch_rows<true, 2, 1, 4, 2, 1024>(p, st);
-        return launch_rows<true, 4, 1, 2, 2, 1024>(p, st);
+            return launch_rows<true, 2, 4, 2>(p, st);
+        return launch_rows<true, 4, 2, 2>(p, st);
     }
     if (p.M <= 16)
-        return launch_rows<false, 1, 1, 4, 2, 1024>(p, st);
+        return launch_rows<false, 1, 4, 2>(p, st);
     if (p.M <= 32)
-        return launch_rows<false, 2, 1, 4, 2, 1024>(p, st);
+        return launch_rows<false, 2, 4, 2>(p, st);
     if (p.M <= 48)
-        return launch_rows<false, 3, 1, 4, 1, 1024>(p, st);
-    return launch_rows<false, 4, 1, 4, 1, 1024>(p, st);
+        return launch_rows<false, 3, 4, 1>(p, st);
+    return launch_rows<false, 4, 4, 1>(p, st);
 }
 
 }  // namespace lora
