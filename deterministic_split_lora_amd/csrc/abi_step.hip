@@ -90,14 +90,6 @@ int check_linear_sizes(int64_t M, int64_t K, int64_t N, int32_t split_k)
     return LORA_OK;
 }
 
-// What lora_mx4_linear_workspace_bytes promises: enough for either kind of x.
-size_t linear_workspace(int64_t M, int64_t K, int64_t N, int32_t split_k)
-{
-    const int64_t a = mx4_linear_workspace(M, N, (int32_t)(K / split_k), split_k, false);
-    const int64_t b = mx4_linear_workspace(M, N, (int32_t)(K / split_k), split_k, true);
-    return (size_t)(a > b ? a : b);
-}
-
 // The checks and the launch behind both products.
 int linear(const void* x, int64_t ld_x, const uint8_t* xs, int64_t ld_xs, const uint8_t* wq, int64_t ld_wq,
            const uint8_t* ws, int64_t ld_ws, uint16_t* y, int64_t ld_y, int64_t M, int64_t K, int64_t N,
@@ -118,7 +110,7 @@ int linear(const void* x, int64_t ld_x, const uint8_t* xs, int64_t ld_xs, const 
         return st;
     if (!aligned(x, 16) || !aligned(y, 16) || ld_y % 8 || (!x_is_mx4 && ld_x % 8) || !aligned(workspace, 16))
         return LORA_ERR_ALIGN;
-    const size_t need = linear_workspace(M, K, N, split_k);
+    const size_t need = mx4_linear_workspace(M, N, (int32_t)(K / split_k), split_k);
     if (need > workspace_bytes)
         return LORA_ERR_WORKSPACE;
     if (need && !workspace)
@@ -173,7 +165,7 @@ size_t lora_mx4_linear_workspace_bytes(int64_t M, int64_t K, int64_t N, int32_t 
 {
     if (check_linear_sizes(M, K, N, split_k) != LORA_OK || M == 0 || N == 0)
         return 0;
-    return linear_workspace(M, K, N, split_k);
+    return mx4_linear_workspace(M, N, (int32_t)(K / split_k), split_k);
 }
 
 int lora_mx4_linear(const uint16_t* x, int64_t ld_x, const uint8_t* wq, int64_t ld_wq, const uint8_t* ws,

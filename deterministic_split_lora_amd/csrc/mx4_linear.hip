@@ -276,26 +276,38 @@ __global__ void __launch_bounds__(256) k_mx4_linear_join(Mx4LinearParams p)
 }
 
 template <bool XMX, int TM, int TN>
-hipError_t launch_split_tile(const Mx4LinearParams& p, hipStream_t st)
+hipError_t launch_split_tile(const Mx4LinearParams& p, int unit, hipStream_t st)
 {
-    const hipError_t e = launch_tile<XMX, TM, TN, kPartial>(p, st);
+    const hipError_t e = launch_tile<XMX, TM, TN, kPartial>(p, unit, st);
     if (e != hipSuccess)
         return e;
     hipLaunchKernelGGL(k_mx4_linear_join, dim3((unsigned)((p.M * (p.N / 8) + 255) / 256)), dim3(256), 0, st, p);
     return hipGetLastError();
 }
 
+// The bytes of a row's scales that the tile kernel loads together: 16 where rows
+// are aligned to them and every chunk starts at a word of scales, otherwise 4.
+int scale_unit(const Mx4LinearParams& p, bool mx)
+{
+    const uintptr_t rows = reinterpret_cast<uintptr_t>(p.ws) | (uintptr_t)p.ld_ws |
+                           (mx ? reinterpret_cast<uintptr_t>(p.xs) | (uintptr_t)p.ld_xs : 0);
+    return rows % 16 == 0 && (p.split_k == 1 || p.k_chunk % 128 == 0) ? 16 : 4;
+}
+
 // Which kernel a call takes: the one of least estimated time.  The estimates, in
-// ns, come from measurements on MI355X (K, N of 4096 .. 28672, M of 1 .. 4096, every
-// split_k) and are within about 20% of them:
+// ns, come from measurements on MI355X:
 //   rows    a chain's steps of 128 k follow one another, and a CU shares its waves'
 //           loads: by tiles of 16 tokens, one step alone / per CU
 //   tiles   a workgroup a CU (two of the small tiles), steps of 128 k one after
-//           another
+//           another; a step costs more where scales come 4 bytes at a time
 //   split   the small tiles, a chunk a workgroup, then the joining launch, which
 //           moves 8 bytes an output and chunk
 // e.g. bf16 x, 200 x 4096 x 6144, split_k 4: 64 x 128 tiles 24.7 us, split 31, rows
 // 85, 128 x 256 tiles 56; 33 x 14336 x 4096, split_k 8: split 17.7, rows 36.5.
+// Over 294 calls (K 2720 .. 14336, M 33 .. 4096, N 4096 .. 8192, split_k 1 .. 8,
+// either unit of scales, either x) the kernel chosen took 0.4% longer than the
+// fastest one on average and 12% at most, and nine of ten estimates of it were
+// within 28%.
 enum Schedule { kRows, kSplit, kTileSmall, kTileMiddle, kTileLarge };
 
 constexpr int64_t kCus = 256;
@@ -305,9 +317,10 @@ int64_t ceil_div(int64_t a, int64_t b)
     return (a + b - 1) / b;
 }
 
-Schedule schedule_for(int64_t M, int64_t N, int32_t k_chunk, int32_t split_k, bool mx)
+Schedule schedule_for(int64_t M, int64_t N, int32_t k_chunk, int32_t split_k, bool mx, int unit)
 {
     const int64_t chunk_steps = ceil_div(k_chunk, kStepK), steps = chunk_steps * split_k;
+    const bool narrow = unit == 4;
     // rows: blocks of up to 64 tokens
     const int64_t alone[2][4] = {{600, 1050, 1600, 2250}, {300, 430, 680, 680}};
     const int64_t shared[2][4] = {{180, 300, 400, 540}, {100, 125, 190, 190}};
@@ -328,13 +341,17 @@ Schedule schedule_for(int64_t M, int64_t N, int32_t k_chunk, int32_t split_k, bo
     const int64_t small_tiles = ceil_div(M, mx ? 128 : 64) * ceil_div(N, 128);
     auto small = [&](int64_t copies) {
         const int64_t n = small_tiles * copies, rest = n % (2 * kCus);
-        const int64_t alone1 = mx ? 520 : 770, paired = mx ? 900 : 1100;
+        const int64_t alone1 = mx ? 520 : 770, paired = mx ? (narrow ? 1250 : 900) : (narrow ? 1320 : 1100);
         return n / (2 * kCus) * paired + (rest > kCus ? paired : rest > 0 ? alone1 : 0);
     };
     consider(kTileSmall, 2000 + small(1) * steps);
-    consider(kTileMiddle, 2000 + rounds(128, 256) * steps * (mx ? 790 : split_k > 1 ? 1750 : 1650));
+    if (split_k == 1 || !narrow)
+        consider(kTileMiddle,
+                 2000 + rounds(128, 256) * steps * (mx ? (narrow ? 900 : 790) : narrow ? 1700 : split_k > 1 ? 1750 : 1650));
+    else if (!mx)                            // the middle tile is 128 x 128 then
+        consider(kTileMiddle, 2000 + rounds(128, 128) * steps * 1100);
     if (mx && split_k == 1)
-        consider(kTileLarge, 2000 + rounds(256, 256) * steps * 1200);
+        consider(kTileLarge, 2000 + rounds(256, 256) * steps * (narrow ? 1250 : 1200));
     if (split_k > 1)
         consider(kSplit, 6500 + small(split_k) * chunk_steps + M * N * split_k * 8 / 4500);
     return best;
@@ -342,27 +359,39 @@ Schedule schedule_for(int64_t M, int64_t N, int32_t k_chunk, int32_t split_k, bo
 
 }  // namespace
 
-int64_t mx4_linear_workspace(int64_t M, int64_t N, int32_t k_chunk, int32_t split_k, bool x_is_mx4)
+int64_t mx4_linear_workspace(int64_t M, int64_t N, int32_t k_chunk, int32_t split_k)
 {
-    return schedule_for(M, N, k_chunk, split_k, x_is_mx4) == kSplit ? M * N * split_k * (int64_t)sizeof(float) : 0;
+    for (int i = 0; i < 4; ++i)
+        if (schedule_for(M, N, k_chunk, split_k, i & 1, i & 2 ? 16 : 4) == kSplit)
+            return M * N * split_k * (int64_t)sizeof(float);
+    return 0;
 }
 
 hipError_t launch_mx4_linear(const Mx4LinearParams& p, bool x_is_mx4, hipStream_t st)
 {
     const bool one = p.split_k == 1;
-    switch (schedule_for(p.M, p.N, p.k_chunk, p.split_k, x_is_mx4)) {
+    const int unit = scale_unit(p, x_is_mx4);
+    switch (schedule_for(p.M, p.N, p.k_chunk, p.split_k, x_is_mx4, unit)) {
     case kSplit:
-        return x_is_mx4 ? launch_split_tile<true, 128, 128>(p, st) : launch_split_tile<false, 64, 128>(p, st);
+        return x_is_mx4 ? launch_split_tile<true, 128, 128>(p, unit, st) : launch_split_tile<false, 64, 128>(p, unit, st);
     case kTileSmall:
         if (x_is_mx4)
-            return one ? launch_tile<true, 128, 128, kOneChunk>(p, st) : launch_tile<true, 128, 128, kAllChunks>(p, st);
-        return one ? launch_tile<false, 64, 128, kOneChunk>(p, st) : launch_tile<false, 64, 128, kAllChunks>(p, st);
+            return one ? launch_tile<true, 128, 128, kOneChunk>(p, unit, st)
+                       : launch_tile<true, 128, 128, kAllChunks>(p, unit, st);
+        return one ? launch_tile<false, 64, 128, kOneChunk>(p, unit, st)
+                   : launch_tile<false, 64, 128, kAllChunks>(p, unit, st);
     case kTileMiddle:
-        if (x_is_mx4)
-            return one ? launch_tile<true, 128, 256, kOneChunk>(p, st) : launch_tile<true, 128, 256, kAllChunks>(p, st);
-        return one ? launch_tile<false, 128, 256, kOneChunk>(p, st) : launch_tile<false, 128, 256, kAllChunks>(p, st);
+        if (one)
+            return x_is_mx4 ? launch_tile<true, 128, 256, kOneChunk>(p, unit, st)
+                            : launch_tile<false, 128, 256, kOneChunk>(p, unit, st);
+        // totals beside the sums and ragged chunks: 256 columns have no registers left
+        // (for MX4 x, 128 are the small tile)
+        if (unit == 4)
+            return launch_tile_unit<false, 128, 128, kAllChunks, 4>(p, st);
+        return x_is_mx4 ? launch_tile_unit<true, 128, 256, kAllChunks, 16>(p, st)
+                        : launch_tile_unit<false, 128, 256, kAllChunks, 16>(p, st);
     case kTileLarge:
-        return launch_tile<true, 256, 256, kOneChunk>(p, st);
+        return launch_tile<true, 256, 256, kOneChunk>(p, unit, st);
     default:
         break;
     }

@@ -517,16 +517,11 @@ hipError_t launch_tile_unit(const Mx4LinearParams& p, hipStream_t st)
     return hipGetLastError();
 }
 
+// By the bytes of scales that are loaded together (scale_unit).
 template <bool XMX, int TM, int TN, TileMode MODE>
-hipError_t launch_tile(const Mx4LinearParams& p, hipStream_t st)
+hipError_t launch_tile(const Mx4LinearParams& p, int unit, hipStream_t st)
 {
-    const uintptr_t rows = reinterpret_cast<uintptr_t>(p.ws) | (uintptr_t)p.ld_ws |
-                           (XMX ? reinterpret_cast<uintptr_t>(p.xs) | (uintptr_t)p.ld_xs : 0);
-    if (rows % 16 == 0 && (p.split_k == 1 || p.k_chunk % 128 == 0))
-        return launch_tile_unit<XMX, TM, TN, MODE, 16>(p, st);
-    // totals beside the sums and ragged chunks: the wide tile has no registers left
-    constexpr int kTN = MODE == kAllChunks && TN == 256 ? 128 : TN;
-    return launch_tile_unit<XMX, TM, kTN, MODE, 4>(p, st);
+    return unit == 16 ? launch_tile_unit<XMX, TM, TN, MODE, 16>(p, st) : launch_tile_unit<XMX, TM, TN, MODE, 4>(p, st);
 }
 
 }  // namespace lora

@@ -44,8 +44,9 @@ struct Mx4LinearParams {
     int32_t split_k;
 };
 
-// Bytes of workspace launch_mx4_linear takes for these sizes (0: none).
-int64_t mx4_linear_workspace(int64_t M, int64_t N, int32_t k_chunk, int32_t split_k, bool x_is_mx4);
+// Bytes of workspace launch_mx4_linear may take for these sizes (0: none), with
+// either kind of x and any alignment of the scales.
+int64_t mx4_linear_workspace(int64_t M, int64_t N, int32_t k_chunk, int32_t split_k);
 hipError_t launch_mx4_linear(const Mx4LinearParams& p, bool x_is_mx4, hipStream_t st);
 
 struct NormParams {
