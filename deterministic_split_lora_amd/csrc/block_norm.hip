@@ -11,8 +11,10 @@
 // then the waves in ascending order.  Threads and VPT follow from C alone, so a
 // row's bits do not depend on the other rows.  As many threads as the row has
 // groups (up to 1024), because a single token's latency is two reductions:
-// measured on MI355X, 1 x 8192 in 4.2 us, 4096 x 8192 with a gate per token in
-// 65.8 us (335 MB, 5.1 TB/s, a large copy's rate).
+// measured on MI355X, 1 x 8192 in 4.1 us, 4096 x 8192 with a gate per token in
+// 66 us (335 MB, 5.1 TB/s, a large copy's rate).  Between the variants' widths part
+// of a workgroup has no columns: without a gate, 8192 x 2048 24 us, 8192 x 2560 51
+// (3.3 TB/s), 8192 x 4096 54 (5.0), 8192 x 5120 74 (4.6), 8192 x 8192 101 (5.3).
 #include "device.h"
 #include "step_kernels.h"
 

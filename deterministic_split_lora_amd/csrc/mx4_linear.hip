@@ -48,8 +48,8 @@ __device__ __forceinline__ T load_at(const uint8_t* base, uint32_t offset)
 // lane group, whose words the lane groups then exchange (bf16 x).  So do the
 // scales, 64 blocks at a time, which a wave keeps in its part of LDS: read four
 // bytes a row and step they would come from L2 every time, a line each.  Measured
-// on MI355X: 1 x 4096 x 6144 in 8 chunks 7.2 us, MX4 x 16 x 8192 x 8192 in 8
-// chunks 11.4 us (36 MB, 3.2 TB/s).
+// on MI355X: 1 x 4096 x 6144 in 8 chunks 6.7 us, MX4 x 16 x 8192 x 8192 in 8
+// chunks 10.8 us (36 MB, 3.4 TB/s).
 template <bool XMX, int RT, int D, int DX>
 __global__ void __launch_bounds__(kRowsThreads) k_mx4_linear_rows(Mx4LinearParams p, int groups)
 {
@@ -302,8 +302,10 @@ int scale_unit(const Mx4LinearParams& p, bool mx)
 //           another; a step costs more where scales come 4 bytes at a time
 //   split   the small tiles, a chunk a workgroup, then the joining launch, which
 //           moves 8 bytes an output and chunk
-// e.g. bf16 x, 200 x 4096 x 6144, split_k 4: 64 x 128 tiles 24.7 us, split 31, rows
-// 85, 128 x 256 tiles 56; 33 x 14336 x 4096, split_k 8: split 17.7, rows 36.5.
+// e.g. bf16 x, 200 x 4096 x 6144, split_k 4: 64 x 128 tiles 24.9 us, split 26.8, rows
+// 85, 128 x 256 tiles 54; 33 x 14336 x 4096, split_k 8: split 17.5, rows 35.2, 64 x
+// 128 tiles 68; with 4-byte scales 2048 x 11008 x 6144, split_k 4: 128 x 128 tiles
+// 290, 64 x 128 338, split 413.
 // Over 294 calls (K 2720 .. 14336, M 33 .. 4096, N 4096 .. 8192, split_k 1 .. 8,
 // either unit of scales, either x) the kernel chosen took 0.4% longer than the
 // fastest one on average and 12% at most, and nine of ten estimates of it were
@@ -345,9 +347,9 @@ Schedule schedule_for(int64_t M, int64_t N, int32_t k_chunk, int32_t split_k, bo
         return n / (2 * kCus) * paired + (rest > kCus ? paired : rest > 0 ? alone1 : 0);
     };
     consider(kTileSmall, 2000 + small(1) * steps);
+    const int64_t middle = mx ? (narrow ? 900 : 790) : narrow ? 1700 : split_k > 1 ? 1750 : 1650;
     if (split_k == 1 || !narrow)
-        consider(kTileMiddle,
-                 2000 + rounds(128, 256) * steps * (mx ? (narrow ? 900 : 790) : narrow ? 1700 : split_k > 1 ? 1750 : 1650));
+        consider(kTileMiddle, 2000 + rounds(128, 256) * steps * middle);
     else if (!mx)                            // the middle tile is 128 x 128 then
         consider(kTileMiddle, 2000 + rounds(128, 128) * steps * 1100);
     if (mx && split_k == 1)
@@ -373,7 +375,8 @@ hipError_t launch_mx4_linear(const Mx4LinearParams& p, bool x_is_mx4, hipStream_
     const int unit = scale_unit(p, x_is_mx4);
     switch (schedule_for(p.M, p.N, p.k_chunk, p.split_k, x_is_mx4, unit)) {
     case kSplit:
-        return x_is_mx4 ? launch_split_tile<true, 128, 128>(p, unit, st) : launch_split_tile<false, 64, 128>(p, unit, st);
+        return x_is_mx4 ? launch_split_tile<true, 128, 128>(p, unit, st)
+                        : launch_split_tile<false, 64, 128>(p, unit, st);
     case kTileSmall:
         if (x_is_mx4)
             return one ? launch_tile<true, 128, 128, kOneChunk>(p, unit, st)

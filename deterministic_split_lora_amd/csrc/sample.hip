@@ -10,10 +10,25 @@
 // prefix too and is given by its last element.
 //
 // One workgroup owns a row: it reads it once for the maximum and once or twice
-// more for what its settings need.  Bound by memory for a greedy row (256 x
-// 128259 fp32: 25.1 us, 5.2 TB/s), by the vector unit for the others, which take
-// an exponential a logit (49 us; with top-p 77) or gather what may be in the top k
-// (49).  1 x 32000 bf16: 4.9 greedy, 13 top-k, 11 without cuts, 20 top-p.
+// more for what its settings need.  A batch is bound by memory, which every pass
+// reads again.  Measured on MI355X, 256 x 128259 fp32 and the bytes read by the
+// counters: greedy 22 us (132 MB), no cuts 46 (270 MB), top-k 50 47 (264 MB), min-p
+// 67, top-p 75-77 (402 MB, 5.2 TB/s; the vector unit is busy for 57% of the time
+// there and for 47% without cuts).  A row alone waits for one CU's passes: 1 x
+// 32000 bf16 4.9 greedy, 11 no cuts, 13.5 top-k 50, 16 min-p, 19 top-p; 1 x 128259
+// fp32 11, 26, 21, 40, 51.
+//
+// Where a list of the usual paths overflows, sample_any takes the row, in six
+// to eleven more passes: 256 x 128259 447-560 us, 1 x 128259 305-424, 1 x 32000 97-130.
+// That is so
+//   with top-k, where more than kFew logits are no less than the k-th largest of
+//     the threads' maxima: of independent logits from a k of 650 to 700 on (at 400
+//     comparing the gathered ones takes 142 us already, at 600 231); of logits that
+//     fall with the index, as in vocabularies ordered by frequency, for 200; and for
+//     any k where more than kFew are left beside masks of a finite value that cover
+//     all logits of some thread (3000 beside -1e9);
+//   with top-p or min-p, where the bin that is cut holds more than kList logits:
+//     flat rows (normal logits of unit spread, 128259 of them, at temperature 4).
 #include "device.h"
 #include "step_kernels.h"
 
@@ -681,8 +696,10 @@ __device__ __forceinline__ uint64_t share_sum(uint64_t v, int share, uint64_t* w
 }
 
 // Top-k rows: the k-th largest of the threads' own maxima bounds the k-th
-// largest logit from below, and few logits lie above it.  Those are gathered
-// and compared with one another.  False if they are too many.
+// largest logit from below.  The logits in its bin and above are gathered and
+// compared with one another.  False if they are more than kFew, as with a large k,
+// or where the large logits are neighbours or the bins are stretched by a finite
+// mask.
 template <bool BF16>
 __device__ bool sample_top_k(const SampleParams& p, const Settings& c, const Row& r, const Groups<BF16>& G, Fast& s,
                              int64_t row, float mine)

@@ -577,7 +577,8 @@ int lora_mx4_linear_q(const uint8_t* xq, int64_t ld_xq, const uint8_t* xs, int64
  *     t  = post_norm(y[i])                       (y itself for LORA_NORM_NONE)
  *     r' = res_scale * r[i] + gate[i / gate_group] * t
  *     r_out[i] = bf16(r'),   x_out[i] = bf16(pre_norm(r'))
- * in fp32, the pre-norm taken from r' before its rounding.
+ * in fp32 (so the sum of a row's squares has to stay below 3.4e38), the pre-norm
+ * taken from r' before its rounding.
  *     LORA_NORM_RMS    norm(v) = v / sqrt(mean(v^2) + eps) * w + b
  *     LORA_NORM_LAYER  the same of v - mean(v)
  * post_w, pre_w (NULL: 1) and post_b, pre_b (NULL: 0): bf16 [C].  gate: bf16
@@ -613,6 +614,10 @@ int lora_block_norm(const uint16_t* y, int64_t ld_y, int32_t post, const uint16_
  * over the indices up to it exceeds t.  T <= 0 or NaN: the first token of the
  * order.  logprobs[i] = log(w_token / W), the natural logarithm of the
  * probability it was drawn with.
+ * Time: a row is read one to three times; with a top_k of several hundred, with
+ * top_k where more than 1024 logits are near the k-th or left beside a mask of a
+ * finite value (mask with -inf instead), and with top_p or min_p where more than
+ * 4096 have nearly the weight of the cut, up to fourteen times.
  * A row of -inf only: token -1, logprob -inf.  An infinite maximum: the logits
  * equal to it share the weight.
  * logits: [B][ld] bf16 (LORA_LOGITS_BF16) or fp32 (LORA_LOGITS_F32), aligned to
