@@ -61,7 +61,11 @@ Matrix matrix(PyObject* arg, at::ScalarType type, const char* name, bool optiona
         refuse(PyExc_ValueError, "%s must be 2-D", name);
     if (t->stride(1) != 1)
         refuse(PyExc_ValueError, "%s rows must be contiguous (stride(1) == 1)", name);
-    return {t->data_ptr(), t->size(0), t->size(1), t->stride(0)};
+    const int64_t rows = t->size(0), cols = t->size(1), ld = t->stride(0);
+    // a single row's stride means nothing (a transposed column's is 1): where it does
+    // not suit the entry points' rules, the width, to a whole word of scales, does
+    const bool as_it_is = rows > 1 || (ld >= cols && ld % 16 == 0);
+    return {t->data_ptr(), rows, cols, as_it_is ? ld : (cols + 3) / 4 * 4};
 }
 
 void* vector(PyObject* arg, int64_t n, at::ScalarType type, const char* name, bool optional = true)
