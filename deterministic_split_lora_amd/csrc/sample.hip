@@ -26,7 +26,8 @@
 //     comparing the gathered ones takes 142 us already, at 600 231); of logits that
 //     fall with the index, as in vocabularies ordered by frequency, for 200; and for
 //     any k where more than kFew are left beside masks of a finite value that cover
-//     all logits of some thread (3000 beside -1e9);
+//     all logits of some thread (3000 beside -1e9); also where k is above the number
+//     of threads with logits, V / 8 (bf16) or V / 4, and V above kFew;
 //   with top-p or min-p, where the bin that is cut holds more than kList logits:
 //     flat rows (normal logits of unit spread, 128259 of them, at temperature 4).
 #include "device.h"
@@ -50,6 +51,10 @@ struct Row {
     int V;
     float inv_t;
     float lmax;
+    // (l - lmax) inv_t as (half l - half_max) inv_half_t: half is 0.5 where the
+    // temperature is above 1, so that a difference past the largest float keeps its
+    // value where it counts (exact, a power of two; 1 below, where it weighs nothing)
+    float half, half_max, inv_half_t;
 };
 
 // The logit of column i; NaN counts as masked (-inf), -0 as +0 (they tie).
@@ -71,10 +76,7 @@ __device__ __forceinline__ uint32_t weight(const Row& r, float l)
 {
     if (l == r.lmax)
         return 1u << 31;
-    // a difference past the largest float: of halves, whose product is then doubled
-    // (exact, both being powers of two; the temperature is past 2^100 if it counts)
-    const float d = l - r.lmax;
-    const float z = d == -INFINITY ? (0.5f * l - 0.5f * r.lmax) * r.inv_t * 2.0f : d * r.inv_t;
+    const float z = fmaf(l, r.half, -r.half_max) * r.inv_half_t;
     // a masked logit, or one whose exponent is not a number (infinite maximum at
     // an infinite temperature), has no weight
     return l == -INFINITY || !(z == z) ? 0u : __float2uint_rn(expf(z) * kOne);
@@ -709,7 +711,7 @@ __device__ bool sample_top_k(const SampleParams& p, const Settings& c, const Row
     const float lowest = -block_reduce_max(mine == -INFINITY ? -INFINITY : -mine, s.red);
     if (!(r.lmax - lowest < INFINITY))
         return false;
-    float per = lowest < r.lmax ? fminf((kThreads - 1) / (r.lmax - lowest), FLT_MAX) : 0.0f;
+    const float per = lowest < r.lmax ? fminf((kThreads - 1) / (r.lmax - lowest), FLT_MAX) : 0.0f;
     auto at = [&](float l) { return (r.lmax - l) * per; };
     uint32_t* count = reinterpret_cast<uint32_t*>(s.sub);
     count[threadIdx.x] = 0;
@@ -729,13 +731,10 @@ __device__ bool sample_top_k(const SampleParams& p, const Settings& c, const Row
     __syncthreads();
     // with fewer than k maxima the k-th logit may lie below all of them, as far as
     // the type reaches: every logit's place is 0
-    float end_place = (float)(s.pick + 1);
-    if (block_sum(own, s.scan) < (uint64_t)c.k) {
-        per = 0.0f;
-        end_place = 1.0f;
-    }
+    const bool all = block_sum(own, s.scan) < (uint64_t)c.k;
+    const float take_per = all ? 0.0f : per, end_place = all ? 1.0f : (float)(s.pick + 1);
     G.gather(
-        &s.n, [&](float l) { return at(l) < end_place; },      // so is not -inf (NaN or infinite place)
+        &s.n, [&](float l) { return (r.lmax - l) * take_per < end_place; },    // so is not -inf (NaN or infinite)
         [&](uint32_t slot, float l, int i) {
             if (slot < kFew) {
                 s.few[slot] = place(order_key(l), i);
@@ -1025,6 +1024,9 @@ __global__ void __launch_bounds__(kThreads) k_sample(SampleParams p)
         }
         return;
     }
+    r.half = r.inv_t < 1.0f ? 0.5f : 1.0f;
+    r.half_max = r.half * r.lmax;
+    r.inv_half_t = r.inv_t / r.half;
     // also that a difference of logits past the largest float weighs nothing: from
     // 1 / T = 22.2 / 3.4e38 on
     const bool finite = r.lmax < INFINITY && r.inv_t > 1e-37f && r.inv_t < INFINITY;
