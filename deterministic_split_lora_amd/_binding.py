@@ -12,6 +12,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+from typing import Any, NamedTuple
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
 LIBRARY_PATH = os.path.join(_HERE, "liblora_det.so")
@@ -37,6 +38,7 @@ EXPORTED = [
     "lora_sgmv_shrink_atomic", "lora_counted_workspace_bytes",
     "lora_mx4_quantize", "lora_mx4_dequantize", "lora_mx4_linear_workspace_bytes", "lora_mx4_linear",
     "lora_mx4_linear_q", "lora_block_norm", "lora_sample",
+    "lora_kv_append", "lora_kv_attention_chunk", "lora_kv_attention_workspace_bytes", "lora_kv_attention",
 ]
 
 
@@ -114,6 +116,10 @@ def lib():
         L.lora_shrink_expand_counted.restype = ctypes.c_int
         L.lora_shrink_expand_counted.argtypes = [_vp, _i64, _vp, _i64, _vp, _i64, _vp, _i64, _vp, _i64, _i64, _i64,
                                                  _i32, _i64, _i32, _f32, _f32, _vp, _sz, _vp, _sz, _vp]
+        L.lora_kv_attention_chunk.restype = _i64
+        L.lora_kv_attention_chunk.argtypes = [_i64, _i32, _i32, _i64]
+        L.lora_kv_attention_workspace_bytes.restype = _sz
+        L.lora_kv_attention_workspace_bytes.argtypes = [_i64, _i32, _i32, _i32, _i64, _i64, _i64]
         L.lora_shrink_counter_bytes.restype = _sz
         L.lora_shrink_counter_bytes.argtypes = [_i64]
         L.lora_counted_workspace_bytes.restype = _sz
@@ -581,7 +587,7 @@ def _native():
         L = lib()
         m.bind(*(ctypes.cast(getattr(L, name), _vp).value for name in (
             "lora_mx4_quantize", "lora_mx4_dequantize", "lora_mx4_linear", "lora_mx4_linear_q", "lora_block_norm",
-            "lora_sample")))
+            "lora_sample", "lora_kv_append", "lora_kv_attention")))
         # the current stream's address without building a Stream object
         _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
             lambda device: torch.cuda.current_stream(device).cuda_stream)
@@ -658,3 +664,49 @@ def lora_sample(logits, u, tokens, temperature=None, top_k=None, top_p=None, min
     if st:
         raise LoraError(st, "lora_sample")
     return tokens
+
+
+class KvCache(NamedTuple):
+    """One layer's paged cache in 8 bits and the batch's tables, all GPU tensors (include/lora_det.h has the layouts)."""
+    k: Any                    # uint8 [pages, heads, page_size, head_dim]
+    v: Any                    # uint8 [pages, heads, page_size / 16, head_dim, 16]
+    k_scales: Any             # uint8 [pages, heads, page_size / 16]
+    v_scales: Any
+    page_table: Any           # int32 [sequences, pages of the longest], -1 (or any other number that is none): no page
+    seq_lens: Any             # int32 [sequences], with the new tokens
+    cu_tokens: Any            # int32 [sequences + 1]: the rows of a step's tensors that are a sequence's new tokens
+
+
+def lora_kv_append(k, v, cache, q=None, q_out=None, q_norm=None, k_norm=None, rope=None, pairs: bool = False,
+                   eps: float = 1e-6, stream=None):
+    """Appends the new tokens' keys and values ([T, heads, D] bf16, also views of a fused projection's output) to the
+    cache, the keys normed per head (k_norm [D]) and rotated by their position (rope [positions, rope_dim] fp32: cosines,
+    then sines; pairs: neighbours rotate, not halves); q_out = q normed and rotated."""
+    st = (_native_module or _native()).kv_append(k, v, cache, q, q_out, q_norm, k_norm, eps, rope, pairs,
+                                                 _stream_address(stream, k))
+    if st:
+        raise LoraError(st, "lora_kv_append")
+    return q_out
+
+
+def lora_kv_attention_chunk(max_new: int, q_heads: int, heads: int, max_len: int) -> int:
+    """The chunk that lora_kv_attention takes for 0 (0 for invalid sizes)."""
+    return int(lib().lora_kv_attention_chunk(max_new, q_heads, heads, max_len))
+
+
+def lora_kv_attention_workspace_bytes(T: int, q_heads: int, heads: int, head_dim: int, max_new: int, max_len: int,
+                                      chunk: int = 0) -> int:
+    return int(lib().lora_kv_attention_workspace_bytes(T, q_heads, heads, head_dim, max_new, max_len, chunk))
+
+
+def lora_kv_attention(q, cache, out, max_new: int, max_len=None, scale=None, causal: bool = True, window: int = 0,
+                      chunk: int = 0, lse=None, workspace=None, stream=None):
+    """out = attention of q ([T, q_heads, D] bf16) over the cache, lse = its log-sum-exp ([T, q_heads] fp32).  max_new,
+    max_len: the longest run of new tokens and the longest sequence (default: all that the table holds); scale: default
+    1 / sqrt(D); chunk: keys that one workgroup joins on its own (0: by these sizes); workspace: tensor of
+    lora_kv_attention_workspace_bytes, None if that is 0."""
+    st = (_native_module or _native()).kv_attention(q, cache, out, max_new, max_len, scale, causal, window, chunk, lse,
+                                                    workspace, _stream_address(stream, q))
+    if st:
+        raise LoraError(st, "lora_kv_attention")
+    return out

@@ -9,6 +9,9 @@
 
 #include "../../include/lora_det.h"
 
+#include <math.h>
+#include <string>
+
 namespace {
 
 // The C entry points, taken from the library that _binding.py has loaded.
@@ -18,6 +21,8 @@ decltype(&lora_mx4_linear) linear_fn;
 decltype(&lora_mx4_linear_q) linear_q_fn;
 decltype(&lora_block_norm) norm_fn;
 decltype(&lora_sample) sample_fn;
+decltype(&lora_kv_append) kv_append_fn;
+decltype(&lora_kv_attention) kv_attention_fn;
 
 struct Refused {};                           // a Python exception is set
 
@@ -265,16 +270,150 @@ PyObject* sample(PyObject*, PyObject* const* a, Py_ssize_t n)
     });
 }
 
+// A tensor [n, ...] whose inner dimensions are contiguous.
+void* inner(PyObject* arg, at::ScalarType type, std::initializer_list<int64_t> dims, int64_t* ld, const char* name)
+{
+    const at::Tensor* t = tensor(arg, type, name);
+    int64_t want = 1;
+    bool fits = t->dim() == (int64_t)dims.size() + 1;
+    for (int64_t d = (int64_t)dims.size(); fits && d >= 1; --d) {
+        const int64_t size = dims.begin()[d - 1];
+        fits = t->size(d) == size && (size == 1 || t->stride(d) == want);
+        want *= size;
+    }
+    if (!fits) {
+        std::string shape;
+        for (int64_t d : dims)
+            shape += ", " + std::to_string(d);
+        refuse(PyExc_ValueError, "%s must be [n%s], contiguous but for the first dimension", name, shape.c_str());
+    }
+    *ld = t->size(0) > 1 ? t->stride(0) : want;
+    return t->data_ptr();
+}
+
+// A batch of heads [T, heads, D].
+struct Heads {
+    void* p = nullptr;
+    int64_t T = 0, heads = 0, ld = 0;
+};
+
+Heads heads(PyObject* arg, int64_t D, const char* name, bool optional = false)
+{
+    const at::Tensor* t = tensor(arg, kBf16, name, optional);
+    if (!t)
+        return {};
+    if (t->dim() != 3)
+        refuse(PyExc_ValueError, "%s must be [tokens, heads, %lld]", name, (long long)D);
+    Heads h;
+    h.T = t->size(0);
+    h.heads = t->size(1);
+    h.p = inner(arg, kBf16, {h.heads, D}, &h.ld, name);
+    return h;
+}
+
+void same_tokens(int64_t T, const Heads& h, const char* name)
+{
+    if (h.T != T)
+        refuse(PyExc_ValueError, "%s must have %lld tokens, got %lld", name, (long long)T, (long long)h.T);
+}
+
+// A tuple of k, v, k_scales, v_scales, page_table, seq_lens, cu_tokens.
+lora_kv_cache kv_cache(PyObject* arg)
+{
+    if (!PyTuple_Check(arg) || PyTuple_GET_SIZE(arg) != 7)
+        refuse(PyExc_TypeError, "cache must be a KvCache");
+    auto item = [&](int i) { return PyTuple_GET_ITEM(arg, i); };
+    const at::Tensor* k = tensor(item(0), at::kByte, "cache.k");
+    if (k->dim() != 4)
+        refuse(PyExc_ValueError, "cache.k must be [pages, heads, page_size, head_dim]");
+    const int64_t pages = k->size(0), H = k->size(1), P = k->size(2), D = k->size(3);
+    if (P < 16 || P % 16)
+        refuse(PyExc_ValueError, "cache.k: a page must hold blocks of 16 tokens, got %lld tokens", (long long)P);
+    lora_kv_cache c{};
+    c.n_pages = pages;
+    c.heads = narrow(H);
+    c.page_size = narrow(P);
+    c.head_dim = narrow(D);
+    c.k = u8(inner(item(0), at::kByte, {H, P, D}, &c.ld_k, "cache.k"));
+    c.v = u8(inner(item(1), at::kByte, {H, P / 16, D, 16}, &c.ld_v, "cache.v"));
+    c.k_scales = u8(inner(item(2), at::kByte, {H, P / 16}, &c.ld_ks, "cache.k_scales"));
+    c.v_scales = u8(inner(item(3), at::kByte, {H, P / 16}, &c.ld_vs, "cache.v_scales"));
+    for (int i = 1; i < 4; ++i)
+        if (THPVariable_Unpack(item(i)).size(0) != pages)
+            refuse(PyExc_ValueError, "cache.k, v, k_scales and v_scales must have the same pages");
+    const Matrix table = matrix(item(4), at::kInt, "cache.page_table");
+    c.page_table = i32(table.p);
+    c.n_seqs = table.rows;
+    c.max_pages = table.cols;
+    c.ld_table = table.rows > 1 ? table.ld : table.cols;
+    c.seq_lens = i32(vector(item(5), table.rows, at::kInt, "cache.seq_lens", false));
+    c.cu_tokens = i32(vector(item(6), table.rows + 1, at::kInt, "cache.cu_tokens", false));
+    return c;
+}
+
+// k, v, cache, q, q_out, q_norm, k_norm, eps, rope, pairs, stream
+PyObject* kv_append(PyObject*, PyObject* const* a, Py_ssize_t n)
+{
+    return call(n, 11, [&] {
+        const lora_kv_cache c = kv_cache(a[2]);
+        const int64_t D = c.head_dim;
+        const Heads k = heads(a[0], D, "k"), v = heads(a[1], D, "v");
+        const Heads q = heads(a[3], D, "q", true), q_out = heads(a[4], D, "q_out", true);
+        same_tokens(k.T, v, "v");
+        if (k.heads != c.heads || v.heads != c.heads)
+            refuse(PyExc_ValueError, "k and v must have the cache's %lld heads", (long long)c.heads);
+        if ((a[3] == Py_None) != (a[4] == Py_None))
+            refuse(PyExc_ValueError, "q and q_out go together");
+        if (a[3] != Py_None) {
+            same_tokens(k.T, q, "q");
+            same_tokens(k.T, q_out, "q_out");
+            if (q.heads != q_out.heads)
+                refuse(PyExc_ValueError, "q and q_out must have the same heads");
+        }
+        const Matrix rope = matrix(a[8], at::kFloat, "rope", true);
+        const int64_t ld_rope = rope.rows > 1 ? rope.ld : rope.cols;
+        return kv_append_fn(&c, u16(q.p), q.ld, u16(q_out.p), q_out.ld, narrow(q.heads), u16(k.p), k.ld, u16(v.p),
+                            v.ld, k.T, u16(vector(a[5], D, kBf16, "q_norm")), u16(vector(a[6], D, kBf16, "k_norm")),
+                            (float)number(a[7]), f32(rope.p), ld_rope, rope.rows, narrow(rope.cols),
+                            narrow(integer(a[9])), address(a[10]));
+    });
+}
+
+// q, cache, out, max_new, max_len (None: the table's), scale (None: 1 / sqrt(D)), causal,
+// window, chunk, lse, workspace, stream
+PyObject* kv_attention(PyObject*, PyObject* const* a, Py_ssize_t n)
+{
+    return call(n, 12, [&] {
+        const lora_kv_cache c = kv_cache(a[1]);
+        const Heads q = heads(a[0], c.head_dim, "q"), out = heads(a[2], c.head_dim, "out");
+        same_tokens(q.T, out, "out");
+        if (q.heads != out.heads)
+            refuse(PyExc_ValueError, "out must have q's heads");
+        const Matrix lse = matrix(a[9], at::kFloat, "lse", true);
+        if (a[9] != Py_None && (lse.rows != q.T || lse.cols != q.heads))
+            refuse(PyExc_ValueError, "lse must be [%lld, %lld]", (long long)q.T, (long long)q.heads);
+        const int64_t capacity = c.max_pages * c.page_size;
+        const int64_t max_len = a[4] == Py_None ? capacity : integer(a[4]);
+        const float scale = a[5] == Py_None ? 1.0f / sqrtf((float)c.head_dim) : (float)number(a[5]);
+        const Workspace w = workspace(a[10]);
+        return kv_attention_fn(&c, u16(q.p), q.ld, u16(out.p), out.ld, f32(lse.p), lse.rows > 1 ? lse.ld : q.heads,
+                               q.T, narrow(q.heads), integer(a[3]), max_len, scale, narrow(integer(a[6])),
+                               integer(a[7]), integer(a[8]), w.p, w.bytes, address(a[11]));
+    });
+}
+
 // The addresses of the entry points, in the order above.
 PyObject* bind(PyObject*, PyObject* const* a, Py_ssize_t n)
 {
-    return call(n, 6, [&] {
+    return call(n, 8, [&] {
         quantize_fn = reinterpret_cast<decltype(quantize_fn)>(address(a[0]));
         dequantize_fn = reinterpret_cast<decltype(dequantize_fn)>(address(a[1]));
         linear_fn = reinterpret_cast<decltype(linear_fn)>(address(a[2]));
         linear_q_fn = reinterpret_cast<decltype(linear_q_fn)>(address(a[3]));
         norm_fn = reinterpret_cast<decltype(norm_fn)>(address(a[4]));
         sample_fn = reinterpret_cast<decltype(sample_fn)>(address(a[5]));
+        kv_append_fn = reinterpret_cast<decltype(kv_append_fn)>(address(a[6]));
+        kv_attention_fn = reinterpret_cast<decltype(kv_attention_fn)>(address(a[7]));
         return 0;
     });
 }
@@ -293,6 +432,8 @@ PyMethodDef methods[] = {
     {"mx4_linear_q", fast(linear_q), METH_FASTCALL, nullptr},
     {"block_norm", fast(block_norm), METH_FASTCALL, nullptr},
     {"sample", fast(sample), METH_FASTCALL, nullptr},
+    {"kv_append", fast(kv_append), METH_FASTCALL, nullptr},
+    {"kv_attention", fast(kv_attention), METH_FASTCALL, nullptr},
     {nullptr, nullptr, 0, nullptr}};
 
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "_native", nullptr, -1, methods, nullptr, nullptr, nullptr, nullptr};

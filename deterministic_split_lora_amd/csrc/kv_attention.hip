@@ -1,0 +1,506 @@
+// Attention over the paged cache in 8 bits.
+//
+// The queries of a sequence that share a key head form rows, r = token * G + member
+// of the group; a wave has tiles of 16 rows as the columns of its matrix products:
+//   S^T = K Q^T     a step's 64 keys x 16 rows, four products of 16 keys
+//   O^T += V^T P^T  D x 16 rows, reduced over the step's 64 keys
+// and keeps for each row the maximum m and the sum l of the softmax (base 2).
+// Key rows are dealt to the products so that lane group g (16 lanes) gets the S
+// of the step's block g, all 16 tokens: these are the P it then supplies, and the
+// tokens of the 16 bytes of V that it loads.  No value changes lanes but for the
+// row's maximum and sum.  Codes become bf16 (exactly) on the way from the load to
+// the product, times their block's scale.
+#include "kv_cache.h"
+
+#include <math.h>
+
+namespace lora {
+
+namespace {
+
+constexpr int kStep = 64;                    // keys a wave takes at a time
+constexpr int kWaves = 4;
+constexpr float kLog2e = 1.44269504088896340736f;
+constexpr float kLn2 = 0.69314718055994530942f;
+
+typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
+
+// Eight codes times a power of two.
+__device__ __forceinline__ bf16x8 widen(uint32_t lo, uint32_t hi, float scale)
+{
+    const bf16x2 a = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(lo, scale, false);
+    const bf16x2 b = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(lo, scale, true);
+    const bf16x2 c = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(hi, scale, false);
+    const bf16x2 d = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(hi, scale, true);
+    return bf16x8{a[0], a[1], b[0], b[1], c[0], c[1], d[0], d[1]};
+}
+
+// Of each byte that is a NaN code the top bit, of others 0.
+__device__ __forceinline__ uint32_t nan_bytes(uint32_t codes)
+{
+    return ((codes & 0x7F7F7F7Fu) + 0x01010101u) & 0x80808080u;
+}
+
+__device__ __forceinline__ float group_max(float v)
+{
+    v = fmaxf(v, __shfl_xor(v, 16));
+    return fmaxf(v, __shfl_xor(v, 32));
+}
+
+__device__ __forceinline__ float group_sum(float v)
+{
+    v += __shfl_xor(v, 16);
+    return v + __shfl_xor(v, 32);
+}
+
+// A logit's place under a maximum that may be -inf (no key yet).
+__device__ __forceinline__ float shift_of(float m)
+{
+    return m == -INFINITY ? 0.0f : m;
+}
+
+struct Work {
+    int64_t b;                               // sequence
+    int64_t row0;                            // first row of the tile
+    int rows;                                // rows of the tile, 0: nothing to do
+    KvSequence s;
+};
+
+// Rows of the sequences lie in tiles of R; tiles of a sequence begin at a slot that
+// grows with it.
+template <int R>
+__device__ __forceinline__ Work find_work(const KvAttentionParams& p, int64_t slot, int G)
+{
+    auto at = [&](int64_t j, int64_t cu) { return cu * G / R + j; };
+    Work w{};
+    w.b = kv_find(p.cache, slot, at);
+    if (w.b >= p.cache.n_seqs)
+        return w;
+    w.s = kv_sequence(p.cache, w.b, p.T);
+    w.row0 = (slot - at(w.b, w.s.first)) * R;
+    const int64_t left = w.s.n * G - w.row0;
+    w.rows = w.row0 >= 0 && left > 0 ? (int)min(left, (int64_t)R) : 0;
+    return w;
+}
+
+// The keys that a row sees: lo .. hi.
+struct Seen {
+    int32_t lo, hi;
+};
+
+__device__ __forceinline__ Seen seen_by(const KvAttentionParams& p, const KvSequence& s, int64_t token)
+{
+    const int64_t end = min(s.len, p.max_len);
+    const int64_t pos = s.len - s.n + token;
+    const int64_t hi = p.causal ? min(pos, end - 1) : end - 1;
+    const int64_t lo = p.window ? max(pos - p.window + 1, (int64_t)0) : 0;
+    return {(int32_t)lo, (int32_t)max(hi, (int64_t)-1)};
+}
+
+__host__ __device__ constexpr int64_t partial_floats(int D) { return D + 4; }
+
+// Split: the waves share the tile's rows and deal out the steps of the chunk;
+// otherwise every wave has rows of its own and takes all steps.
+template <int D, int NT, bool SPLIT>
+__global__ void __launch_bounds__(kWaves * 64) k_attention(KvAttentionParams p, uint32_t slots)
+{
+    constexpr int R = 16 * NT * (SPLIT ? 1 : kWaves);
+    constexpr int kLoads = D / 64;           // 16-byte loads of a key by its 4 lanes
+    constexpr int kOut = D / 16;             // tiles of 16 d
+    const int H = p.cache.heads, G = p.q_heads / H;
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, li = lane & 15, g = lane >> 4;
+    const int head = (int)(blockIdx.x % (uint32_t)H);
+    const uint32_t tile = blockIdx.x / (uint32_t)H;
+    const int64_t slot = tile % slots, chunk = tile / slots;
+
+    const Work w = find_work<R>(p, slot, G);
+    if (w.rows == 0)
+        return;
+    // rows of all sequences fit 31 bits
+    const int first_token = (int)w.row0 / G, last_token = ((int)w.row0 + w.rows - 1) / G;
+    const Seen first = seen_by(p, w.s, first_token), last = seen_by(p, w.s, last_token);
+    const int64_t begin = max(chunk * p.chunk, (int64_t)first.lo / kStep * kStep);
+    const int64_t end = min((chunk + 1) * p.chunk, (int64_t)last.hi + 1);
+    const bool several = p.partial != nullptr;
+    if (several && begin >= end)
+        return;
+
+    // the rows of this lane's columns
+    int64_t row_at[NT];                      // token's row of q and out
+    int row_head[NT];
+    Seen seen[NT];
+    bf16x8 q[NT][2 * kLoads];
+#pragma unroll
+    for (int n = 0; n < NT; ++n) {
+        const int r = (SPLIT ? 0 : wave * NT * 16) + n * 16 + li;
+        const bool in = r < w.rows;
+        const int row = (int)w.row0 + (in ? r : 0), token = row / G;
+        row_at[n] = in ? w.s.first + token : -1;
+        row_head[n] = head * G + row - token * G;
+        seen[n] = seen_by(p, w.s, token);
+        if (!in)
+            seen[n].hi = -1;
+        const uint16_t* src = p.q + (w.s.first + token) * p.ld_q + (int64_t)row_head[n] * D + 16 * g;
+#pragma unroll
+        for (int j = 0; j < kLoads; ++j) {
+            q[n][2 * j] = load_bf16x8(src + 64 * j);
+            q[n][2 * j + 1] = load_bf16x8(src + 64 * j + 8);
+        }
+    }
+
+    f32x4 o[NT][kOut];
+    float m[NT], l[NT];                      // l: of this lane's keys
+#pragma unroll
+    for (int n = 0; n < NT; ++n) {
+        m[n] = -INFINITY;
+        l[n] = 0.0f;
+#pragma unroll
+        for (int d = 0; d < kOut; ++d)
+            o[n][d] = f32x4{0, 0, 0, 0};
+    }
+    const float sl = p.scale * kLog2e;
+    const int P = p.cache.page_size;
+
+    int64_t s0 = begin / kStep;
+    if (SPLIT)
+        s0 += (wave - (int)(s0 % kWaves) + kWaves) % kWaves;
+    for (int64_t step = s0; step * kStep < end; step += SPLIT ? kWaves : 1) {
+        const int64_t p0 = step * kStep;
+        // keys: this lane's row of the products is of block li / 4; values: of block g
+        const int64_t pk = p0 + li / 4 * kKvBlock, pv = p0 + g * kKvBlock;
+        const int32_t page_k = kv_page(p.cache, w.b, pk), page_v = kv_page(p.cache, w.b, pv);
+        const int64_t ik = max(page_k, 0), iv = max(page_v, 0);
+        const int wk = (int)(pk & (P - 1)), wv = (int)(pv & (P - 1));
+        const uint8_t* kp = p.cache.k + ik * p.cache.ld_k + ((int64_t)head * P + wk + li % 4) * D + 16 * g;
+        const uint8_t* vp = p.cache.v + iv * p.cache.ld_v + ((int64_t)head * P + wv) * D + 16 * li;
+        const float ks = pow2_of_scale(p.cache.k_scales[ik * p.cache.ld_ks + (head * P + wk) / kKvBlock]);
+        float vs = pow2_of_scale(p.cache.v_scales[iv * p.cache.ld_vs + (head * P + wv) / kKvBlock]);
+        u32x4 kc[4][kLoads], vc[kOut];
+#pragma unroll
+        for (int t = 0; t < 4; ++t)
+#pragma unroll
+            for (int j = 0; j < kLoads; ++j)
+                kc[t][j] = *(const global_u32x4*)(kp + 4 * t * D + 64 * j);
+#pragma unroll
+        for (int d = 0; d < kOut; ++d)
+            vc[d] = *(const global_u32x4*)(vp + 16 * 16 * d);
+
+        f32x4 s[NT][4];
+#pragma unroll
+        for (int t = 0; t < 4; ++t) {
+#pragma unroll
+            for (int n = 0; n < NT; ++n)
+                s[n][t] = f32x4{0, 0, 0, 0};
+#pragma unroll
+            for (int j = 0; j < kLoads; ++j) {
+                const bf16x8 k0 = widen(kc[t][j][0], kc[t][j][1], ks), k1 = widen(kc[t][j][2], kc[t][j][3], ks);
+#pragma unroll
+                for (int n = 0; n < NT; ++n) {
+                    s[n][t] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(k0, q[n][2 * j], s[n][t], 0, 0, 0);
+                    s[n][t] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(k1, q[n][2 * j + 1], s[n][t], 0, 0, 0);
+                }
+            }
+        }
+
+        // every row of the tile sees every key of most steps
+        const bool edge = p0 < last.lo || p0 + kStep - 1 > first.hi || __any(page_v < 0);
+        uint32_t bad = 0;
+        if (edge) {
+#pragma unroll
+            for (int n = 0; n < NT; ++n)
+#pragma unroll
+                for (int t = 0; t < 4; ++t)
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        const int key = (int)pv + 4 * t + i;
+                        const bool in = page_v >= 0 && key >= seen[n].lo && key <= seen[n].hi;
+                        s[n][t][i] = in ? s[n][t][i] : -INFINITY;
+                    }
+            // a block that was never written may hold anything, its scale too
+            const bool unseen = page_v < 0 || pv > last.hi;
+            vs = unseen ? 1.0f : vs;
+#pragma unroll
+            for (int d = 0; d < kOut; ++d)
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    vc[d][i] = unseen ? 0u : vc[d][i];
+                    bad |= nan_bytes(vc[d][i]);
+                }
+        }
+        bf16x8 prob[NT][2];
+#pragma unroll
+        for (int n = 0; n < NT; ++n) {
+            float top = -INFINITY;
+#pragma unroll
+            for (int t = 0; t < 4; ++t)
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                    top = fmaxf(top, s[n][t][i]);
+            const float mn = fmaxf(m[n], group_max(top) * sl);
+            const float shift = shift_of(mn), f = exp2f(m[n] - shift);
+            m[n] = mn;
+            float sum = 0.0f;
+#pragma unroll
+            for (int t = 0; t < 4; ++t)
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const float e = __builtin_amdgcn_exp2f(fmaf(s[n][t][i], sl, -shift));
+                    sum += e;
+                    prob[n][t / 2][4 * (t % 2) + i] = (__bf16)e;
+                }
+            l[n] = l[n] * f + sum;
+#pragma unroll
+            for (int d = 0; d < kOut; ++d)
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                    o[n][d][i] *= f;
+        }
+        if (edge && __any(bad != 0)) {
+            // a value that is NaN reaches the rows that see its key, and no others
+#pragma unroll
+            for (int n = 0; n < NT; ++n) {
+                bf16x8 sees[2];
+#pragma unroll
+                for (int t = 0; t < 4; ++t)
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        const int key = (int)pv + 4 * t + i;
+                        const bool in = page_v >= 0 && key >= seen[n].lo && key <= seen[n].hi;
+                        sees[t / 2][4 * (t % 2) + i] = in ? (__bf16)1.0f : (__bf16)0.0f;
+                    }
+#pragma unroll
+                for (int d = 0; d < kOut; ++d) {
+                    f32x4 hit = {0, 0, 0, 0};
+#pragma unroll
+                    for (int u = 0; u < 2; ++u) {
+                        const bf16x8 one =
+                            widen(nan_bytes(vc[d][2 * u]) >> 7 << 5 & 0x20202020u,
+                                  nan_bytes(vc[d][2 * u + 1]) >> 7 << 5 & 0x20202020u, 1.0f);
+                        hit = __builtin_amdgcn_mfma_f32_16x16x32_bf16(one, sees[u], hit, 0, 0, 0);
+                    }
+#pragma unroll
+                    for (int i = 0; i < 4; ++i)
+                        o[n][d][i] = hit[i] > 0.0f ? __builtin_nanf("") : o[n][d][i];
+                }
+            }
+#pragma unroll
+            for (int d = 0; d < kOut; ++d)
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const uint32_t b = nan_bytes(vc[d][i]);
+                    vc[d][i] &= ~((b >> 7) * 0xFFu);
+                }
+        }
+#pragma unroll
+        for (int d = 0; d < kOut; ++d) {
+            const bf16x8 v0 = widen(vc[d][0], vc[d][1], vs), v1 = widen(vc[d][2], vc[d][3], vs);
+#pragma unroll
+            for (int n = 0; n < NT; ++n) {
+                o[n][d] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(v0, prob[n][0], o[n][d], 0, 0, 0);
+                o[n][d] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(v1, prob[n][1], o[n][d], 0, 0, 0);
+            }
+        }
+    }
+#pragma unroll
+    for (int n = 0; n < NT; ++n)
+        l[n] = group_sum(l[n]);
+
+    if constexpr (SPLIT) {
+        // the waves' shares are joined in ascending order
+        __shared__ float ml[kWaves][R][2];
+        __shared__ float ow[kWaves][16][D + 4];
+#pragma unroll
+        for (int n = 0; n < NT; ++n)
+            if (g == 0) {
+                ml[wave][n * 16 + li][0] = m[n];
+                ml[wave][n * 16 + li][1] = l[n];
+            }
+        // unrolled, so that o stays in registers
+#pragma unroll
+        for (int n = 0; n < NT; ++n) {
+            __syncthreads();
+#pragma unroll
+            for (int d = 0; d < kOut; ++d)
+                *reinterpret_cast<f32x4*>(&ow[wave][li][16 * d + 4 * g]) = o[n][d];
+            __syncthreads();
+            // 16 threads a row, each D / 16 values next to one another by fours
+            const int r = threadIdx.x >> 4, c0 = (threadIdx.x & 15) * 4, row = n * 16 + r;
+            if (row < w.rows) {
+                float top = -INFINITY;
+#pragma unroll
+                for (int v = 0; v < kWaves; ++v)
+                    top = fmaxf(top, ml[v][row][0]);
+                const float shift = shift_of(top);
+                float total = 0.0f, f[kWaves];
+#pragma unroll
+                for (int v = 0; v < kWaves; ++v) {
+                    f[v] = exp2f(ml[v][row][0] - shift);
+                    total += ml[v][row][1] * f[v];
+                }
+                const int rr = (int)w.row0 + row, token = rr / G, h = head * G + rr - token * G;
+                const int64_t at = w.s.first + token;
+#pragma unroll
+                for (int c = 0; c < D; c += 64) {
+                    f32x4 x = {0, 0, 0, 0};
+#pragma unroll
+                    for (int v = 0; v < kWaves; ++v) {
+                        const f32x4 y = *reinterpret_cast<const f32x4*>(&ow[v][r][c + c0]);
+#pragma unroll
+                        for (int i = 0; i < 4; ++i)
+                            x[i] += y[i] * f[v];
+                    }
+                    if (several) {
+                        float* dst = p.partial + ((chunk * p.T + at) * p.q_heads + h) * partial_floats(D);
+                        *reinterpret_cast<f32x4*>(dst + 4 + c + c0) = x;
+                        if (c + c0 == 0) {
+                            dst[0] = top;
+                            dst[1] = total;
+                        }
+                    } else {
+                        const float inv = total == 0.0f ? 0.0f : 1.0f / total;
+                        typedef __bf16 bf16x4 __attribute__((ext_vector_type(4)));
+                        *reinterpret_cast<bf16x4*>(p.out + at * p.ld_out + (int64_t)h * D + c + c0) =
+                            bf16x4{(__bf16)(x[0] * inv), (__bf16)(x[1] * inv), (__bf16)(x[2] * inv), (__bf16)(x[3] * inv)};
+                        if (p.lse && c + c0 == 0)
+                            p.lse[at * p.ld_lse + h] = total == 0.0f ? -INFINITY : (top + log2f(total)) * kLn2;
+                    }
+                }
+            }
+        }
+    } else {
+#pragma unroll
+        for (int n = 0; n < NT; ++n) {
+            if (row_at[n] < 0)
+                continue;
+            if (several) {
+                float* dst = p.partial + ((chunk * p.T + row_at[n]) * p.q_heads + row_head[n]) * partial_floats(D);
+#pragma unroll
+                for (int d = 0; d < kOut; ++d)
+                    *reinterpret_cast<f32x4*>(dst + 4 + 16 * d + 4 * g) = o[n][d];
+                if (g == 0) {
+                    dst[0] = m[n];
+                    dst[1] = l[n];
+                }
+            } else {
+                const float inv = l[n] == 0.0f ? 0.0f : 1.0f / l[n];
+                uint16_t* dst = p.out + row_at[n] * p.ld_out + (int64_t)row_head[n] * D;
+                typedef __bf16 bf16x4 __attribute__((ext_vector_type(4)));
+#pragma unroll
+                for (int d = 0; d < kOut; ++d)
+                    *reinterpret_cast<bf16x4*>(dst + 16 * d + 4 * g) =
+                        bf16x4{(__bf16)(o[n][d][0] * inv), (__bf16)(o[n][d][1] * inv), (__bf16)(o[n][d][2] * inv),
+                               (__bf16)(o[n][d][3] * inv)};
+                if (p.lse && g == 0)
+                    p.lse[row_at[n] * p.ld_lse + row_head[n]] =
+                        l[n] == 0.0f ? -INFINITY : (m[n] + log2f(l[n])) * kLn2;
+            }
+        }
+    }
+}
+
+// Joins the chunks of each row in ascending order: D / 4 threads a row, a block for
+// heads of one token.
+template <int D>
+__global__ void __launch_bounds__(256) k_join(KvAttentionParams p)
+{
+    constexpr int kThreads = D / 4, kHeads = 256 / kThreads;
+    const uint32_t groups = ((uint32_t)p.q_heads + kHeads - 1) / kHeads;
+    const int64_t at = blockIdx.x / groups;
+    const int h = (int)(blockIdx.x % groups) * kHeads + threadIdx.x / kThreads;
+    const int c = threadIdx.x % kThreads * 4;
+    const int64_t row = at * p.q_heads + h;
+    const int64_t b = kv_find(p.cache, at, [](int64_t, int64_t cu) { return cu; });
+    if (h >= p.q_heads || b >= p.cache.n_seqs)
+        return;
+    const KvSequence s = kv_sequence(p.cache, b, p.T);
+    if (s.n == 0 || at < s.first)
+        return;
+    const Seen seen = seen_by(p, s, at - s.first);
+    const int64_t c0 = seen.lo / p.chunk, c1 = seen.hi < seen.lo ? c0 : seen.hi / p.chunk + 1;
+    const int64_t pitch = p.T * p.q_heads * partial_floats(D);
+    const float* src = p.partial + row * partial_floats(D);
+    float top = -INFINITY;
+    for (int64_t i = c0; i < c1; ++i)
+        top = fmaxf(top, src[i * pitch]);
+    const float shift = shift_of(top);
+    float total = 0.0f;
+    f32x4 x = {0, 0, 0, 0};
+#pragma unroll 4
+    for (int64_t i = c0; i < c1; ++i) {
+        const float f = exp2f(src[i * pitch] - shift);
+        const f32x4 y = *reinterpret_cast<const f32x4*>(src + i * pitch + 4 + c);
+        total += src[i * pitch + 1] * f;
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+            x[e] += y[e] * f;
+    }
+    const float inv = total == 0.0f ? 0.0f : 1.0f / total;
+    typedef __bf16 bf16x4 __attribute__((ext_vector_type(4)));
+    *reinterpret_cast<bf16x4*>(p.out + at * p.ld_out + (int64_t)h * D + c) =
+        bf16x4{(__bf16)(x[0] * inv), (__bf16)(x[1] * inv), (__bf16)(x[2] * inv), (__bf16)(x[3] * inv)};
+    if (p.lse && c == 0)
+        p.lse[at * p.ld_lse + h] = total == 0.0f ? -INFINITY : (top + log2f(total)) * kLn2;
+}
+
+// Rows of a tile that these sizes get; up to 64 rows a sequence the waves split the keys.
+int tile_rows(int64_t max_new, int G)
+{
+    const int64_t rows = max_new * G;
+    return rows <= 16 ? 16 : rows <= 64 ? 32 : 128;
+}
+
+int64_t tile_slots(int64_t T, int64_t n_seqs, int R, int G)
+{
+    return T * G / R + n_seqs;
+}
+
+template <int D>
+hipError_t launch(const KvAttentionParams& p, hipStream_t st)
+{
+    const int G = p.q_heads / p.cache.heads, R = tile_rows(p.max_new, G);
+    const int64_t slots = tile_slots(p.T, p.cache.n_seqs, R, G);
+    const int64_t chunks = (p.max_len + p.chunk - 1) / p.chunk;
+    const dim3 grid((unsigned)(slots * p.cache.heads * chunks)), threads(kWaves * 64);
+    if (R == 16)
+        hipLaunchKernelGGL((k_attention<D, 1, true>), grid, threads, 0, st, p, (uint32_t)slots);
+    else if (R == 32)
+        hipLaunchKernelGGL((k_attention<D, 2, true>), grid, threads, 0, st, p, (uint32_t)slots);
+    else
+        hipLaunchKernelGGL((k_attention<D, 2, false>), grid, threads, 0, st, p, (uint32_t)slots);
+    if (p.partial) {
+        const int per = 256 / (D / 4);
+        hipLaunchKernelGGL(k_join<D>, dim3((unsigned)(p.T * ((p.q_heads + per - 1) / per))), dim3(256), 0, st, p);
+    }
+    return hipGetLastError();
+}
+
+}  // namespace
+
+int64_t kv_attention_chunk(int64_t max_new, int32_t q_heads, int32_t kv_heads, int64_t max_len)
+{
+    const int G = q_heads / kv_heads, R = tile_rows(max_new, G);
+    const int64_t tiles = (max_new * G + R - 1) / R * kv_heads;
+    const int64_t splits = tiles < 512 ? 512 / tiles : 1;
+    const int64_t chunk = (max_len + splits - 1) / splits;
+    return (chunk + kKvChunkUnit - 1) / kKvChunkUnit * kKvChunkUnit;
+}
+
+int64_t kv_attention_workspace(int64_t T, int32_t q_heads, int32_t D, int64_t max_len, int64_t chunk)
+{
+    const int64_t chunks = (max_len + chunk - 1) / chunk;
+    return chunks > 1 ? chunks * T * q_heads * partial_floats(D) * 4 : 0;
+}
+
+int64_t kv_attention_blocks(int64_t T, int64_t n_seqs, int64_t max_new, int32_t q_heads, int32_t kv_heads,
+                            int64_t max_len, int64_t chunk)
+{
+    const int G = q_heads / kv_heads;
+    return tile_slots(T, n_seqs, tile_rows(max_new, G), G) * kv_heads * ((max_len + chunk - 1) / chunk);
+}
+
+hipError_t launch_kv_attention(const KvAttentionParams& p, hipStream_t st)
+{
+    return p.D == 64 ? launch<64>(p, st) : p.D == 128 ? launch<128>(p, st) : launch<256>(p, st);
+}
+
+}  // namespace lora

@@ -91,4 +91,83 @@ struct SampleParams {
 
 hipError_t launch_sample(const SampleParams& p, bool bf16, hipStream_t st);
 
+constexpr int kKvBlock = 16;                 // tokens that share a scale in the cache
+
+// The paged cache and the batch's tables (kv_cache.h has the layouts).
+struct KvCacheView {
+    uint8_t* k;
+    uint8_t* v;
+    uint8_t* k_scales;
+    uint8_t* v_scales;
+    int64_t ld_k;                   // bytes from page to page
+    int64_t ld_v;
+    int64_t ld_ks;
+    int64_t ld_vs;
+    const int32_t* page_table;      // [n_seqs][ld_table], max_pages used
+    int64_t ld_table;
+    int64_t max_pages;
+    const int32_t* seq_lens;        // [n_seqs]
+    const int32_t* cu_tokens;       // [n_seqs + 1]
+    int64_t n_seqs;
+    int32_t n_pages;
+    int32_t page_size;              // a power of two, 16 at least
+    int32_t page_shift;
+    int32_t heads;                  // of keys and values
+};
+
+struct KvAppendParams {
+    KvCacheView cache;
+    const uint16_t* q;              // may be null: no queries
+    int64_t ld_q;
+    uint16_t* q_out;
+    int64_t ld_qo;
+    const uint16_t* k;
+    int64_t ld_k;
+    const uint16_t* v;
+    int64_t ld_v;
+    const uint16_t* q_norm;         // each may be null: no norm
+    const uint16_t* k_norm;
+    const float* rope;              // may be null: no rotation
+    int64_t ld_rope;
+    int64_t rope_rows;
+    int64_t T;
+    int32_t rope_dim;
+    int32_t pairs;
+    int32_t q_heads;
+    int32_t D;
+    float eps;
+};
+
+hipError_t launch_kv_append(const KvAppendParams& p, hipStream_t st);
+
+struct KvAttentionParams {
+    KvCacheView cache;
+    const uint16_t* q;
+    int64_t ld_q;
+    uint16_t* out;
+    int64_t ld_out;
+    float* lse;                     // may be null
+    int64_t ld_lse;
+    float* partial;                 // workspace of several chunks
+    int64_t T;
+    int64_t max_len;
+    int64_t chunk;                  // keys of a chunk, a multiple of kKvChunkUnit
+    int64_t max_new;
+    int32_t q_heads;
+    int32_t D;
+    int32_t causal;
+    int32_t window;                 // 0: none
+    float scale;
+};
+
+constexpr int kKvChunkUnit = 256;
+
+// The chunk that these sizes get by default.
+int64_t kv_attention_chunk(int64_t max_new, int32_t q_heads, int32_t kv_heads, int64_t max_len);
+// Bytes of workspace (0: one chunk) and blocks of a launch with these sizes.
+int64_t kv_attention_workspace(int64_t T, int32_t q_heads, int32_t D, int64_t max_len, int64_t chunk);
+int64_t kv_attention_blocks(int64_t T, int64_t n_seqs, int64_t max_new, int32_t q_heads, int32_t kv_heads,
+                            int64_t max_len, int64_t chunk);
+hipError_t launch_kv_attention(const KvAttentionParams& p, hipStream_t st);
+
 }  // namespace lora

@@ -632,6 +632,127 @@ int lora_sample(const void* logits, int32_t logits_type, int64_t ld, int64_t B, 
                 const int32_t* top_k, const float* top_p, const float* min_p, const float* u, int32_t* tokens,
                 float* logprobs, void* stream);
 
+/* ---------------------------------------------------------------------------
+ * The paged key / value cache in 8 bits, and attention over it.
+ *
+ * A page holds page_size tokens of every head of one layer, in blocks of 16
+ * tokens.  A block of a head has one E8M0 scale byte for its keys and one for its
+ * values; a value is code * 2^(byte - 127), the codes are E4M3 (1 sign, 4 exponent
+ * and 3 fraction bits, no infinities, 0x7F and 0xFF NaN).  Scale bytes are 1..246.
+ *   k         uint8 [n_pages][heads][page_size][head_dim]
+ *   v         uint8 [n_pages][heads][page_size / 16][head_dim][16]: the tokens of
+ *             a block lie next to one another for each of the head's values
+ *   k_scales, v_scales   uint8 [n_pages][heads][page_size / 16]
+ * ld_k, ld_v, ld_ks, ld_vs: bytes from a page to the next (the inner layout is as
+ * above).  k, v: 16-byte aligned, ld_k % 16 == 0, ld_v % 16 == 0.
+ *
+ * The batch: sequence b (of n_seqs) has seq_lens[b] tokens with its new ones, and
+ * rows cu_tokens[b] .. cu_tokens[b + 1] - 1 of the step's tensors are its new
+ * tokens, its last ones: row i is the token at position
+ *     seq_lens[b] - (cu_tokens[b + 1] - i).
+ * Its tokens [j page_size, (j + 1) page_size) lie in page page_table[b][j].
+ *   page_table  int32 [n_seqs][ld_table], max_pages entries of a row used
+ *   seq_lens    int32 [n_seqs],  cu_tokens int32 [n_seqs + 1], not falling
+ * All are device arrays, read when the kernels run.  A page outside [0, n_pages),
+ * or behind max_pages, is not there: nothing is appended to it, and its tokens are
+ * seen by no query (as after a window has moved past them).  Rows outside
+ * [cu_tokens[0], cu_tokens[n_seqs]) are left as they are.  Sequences may share
+ * pages that none of them appends to.
+ *
+ * page_size a power of two from 16 to 32768; head_dim 64, 128 or 256; heads and
+ * n_seqs at most 65536.
+ * ------------------------------------------------------------------------- */
+typedef struct lora_kv_cache {
+    uint8_t* k;
+    uint8_t* v;
+    uint8_t* k_scales;
+    uint8_t* v_scales;
+    int64_t ld_k, ld_v, ld_ks, ld_vs;
+    int64_t n_pages;
+    int32_t page_size;
+    int32_t heads;
+    int32_t head_dim;
+    const int32_t* page_table;
+    int64_t ld_table;
+    int64_t max_pages;
+    const int32_t* seq_lens;
+    const int32_t* cu_tokens;
+    int64_t n_seqs;
+} lora_kv_cache;
+
+/*
+ * Append the new tokens' keys and values to the cache, and make their queries
+ * ready: norm of each head, rotation by the position, rounding.  With t a head of q
+ * or k in fp32, D = head_dim:
+ *   norm    t / sqrt(mean(t^2) + eps) * w      (q_norm, k_norm bf16 [D]; NULL: none)
+ *   rotate  (a, b) -> (a cos - b sin, b cos + a sin), for j < rope_dim / 2, with
+ *           cos = rope[position][j], sin = rope[position][rope_dim / 2 + j] and the
+ *           values a, b number j and j + rope_dim / 2 of the head (pairs 0), or
+ *           2j and 2j + 1 (pairs 1); values from rope_dim on stay.
+ *           rope: fp32 [rope_rows][ld_rope]; NULL: no rotation.  A position outside
+ *           the table rotates by NaN.
+ * Every operation rounds to fp32 on its own; the sum of squares is taken in fp64.
+ *   q_out = bf16(q rotated);  codes = e4m3(value * 2^(127 - byte)), both to nearest,
+ *   ties to even; infinities become the largest code, NaN stays.
+ * The byte of a block: the least in 27..246 for which no finite value of its tokens
+ * exceeds 448 * 2^(byte - 127) (246 where there is none; what exceeds it becomes the
+ * largest code).  Tokens appended to a block that has earlier
+ * ones keep its byte unless they need a larger one: then the earlier codes are
+ * rounded to the new byte from the values they stand for.  (A first token in a block
+ * begins it anew; what a step leaves in a block behind its last token is unspecified
+ * only if nothing was ever written there.)  So what the cache holds depends on the
+ * sequence's tokens and on where its steps begin, on nothing else.
+ * q, q_out: bf16 [T][ld], q_heads * D columns, or both NULL; q_out may be q with the
+ * same leading dimension.  k, v: bf16 [T][ld], heads * D columns.
+ * 16-byte aligned, leading dimensions multiples of 8 (of rope: 4); rope_dim a
+ * multiple of 16 up to D.  No page may be appended to twice in a call.  One launch.
+ */
+int lora_kv_append(const lora_kv_cache* cache, const uint16_t* q, int64_t ld_q, uint16_t* q_out, int64_t ld_qo,
+                   int32_t q_heads, const uint16_t* k, int64_t ld_k, const uint16_t* v, int64_t ld_v, int64_t T,
+                   const uint16_t* q_norm, const uint16_t* k_norm, float eps, const float* rope, int64_t ld_rope,
+                   int64_t rope_rows, int32_t rope_dim, int32_t pairs, void* stream);
+
+/*
+ * Attention of a step's queries over the cache (the new tokens' keys and values
+ * appended before).  A query at position t of its sequence, of head i, sees the
+ * tokens j of key head i / (q_heads / heads) with
+ *     j <= t (causal), j > t - window (window > 0), j < min(seq_lens, max_len)
+ * that have a page:
+ *     out = sum_j p_j v_j,  p_j = exp(scale q.k_j) / sum_j exp(scale q.k_j)
+ *     lse = log sum_j exp(scale q.k_j)
+ * A query that sees nothing gets 0 and -inf.  A NaN or an infinity in a key or value
+ * that it does not see does not reach it.
+ * Products are exact with fp32 accumulators; maximum, sum and output are held in
+ * fp32, the p_j enter the product with v rounded to bf16 (relative to the largest of
+ * the keys up to there).
+ * Keys are cut into chunks of `chunk` positions, [0, chunk), [chunk, 2 chunk), ..,
+ * which run in parallel and are joined in ascending order in fp32.  chunk: a multiple
+ * of 256, or 0 for lora_kv_attention_chunk's, which suits one sequence with max_new
+ * new tokens and max_len tokens; a large batch runs best with few chunks.  A query's
+ * bits depend on it, its sequence's cache, chunk and max_new's class
+ * (max_new * q_heads / heads up to 16, up to 64, above) only.
+ *   max_new   the longest run of new tokens: it picks the kernel, a longer one is
+ *             served too
+ *   max_len   the longest seq_lens (the grid is made for it; tokens behind are not
+ *             seen).  At most 2^30, and taken as max_pages * page_size where that
+ *             is less
+ * q, out: bf16 [T][ld], q_heads * D columns, 16-byte aligned, ld a multiple of 8;
+ * lse: fp32 [T][ld_lse] or NULL.  window needs causal.  scale: positive, finite.
+ * q_heads a multiple of heads; T * q_heads < 2^31, with several chunks
+ * T * (q_heads * head_dim rounded up to 1024) < 2^34.
+ * workspace: lora_kv_attention_workspace_bytes of the same sizes, 16-byte aligned, no
+ * initialisation needed (NULL where that is 0; 0 is also returned for invalid input).
+ * One launch, two with more than one chunk.
+ */
+int64_t lora_kv_attention_chunk(int64_t max_new, int32_t q_heads, int32_t heads, int64_t max_len);
+size_t lora_kv_attention_workspace_bytes(int64_t T, int32_t q_heads, int32_t heads, int32_t head_dim, int64_t max_new,
+                                         int64_t max_len, int64_t chunk);
+
+int lora_kv_attention(const lora_kv_cache* cache, const uint16_t* q, int64_t ld_q, uint16_t* out, int64_t ld_out,
+                      float* lse, int64_t ld_lse, int64_t T, int32_t q_heads, int64_t max_new, int64_t max_len,
+                      float scale, int32_t causal, int64_t window, int64_t chunk, void* workspace,
+                      size_t workspace_bytes, void* stream);
+
 #ifdef __cplusplus
 }
 #endif
