@@ -17,5 +17,6 @@ from ._binding import (  # noqa: F401
     lora_sgmv_shrink_atomic, lora_counted_workspace_bytes,
     lora_mx4_quantize, lora_mx4_dequantize, lora_mx4_linear, lora_mx4_linear_q, lora_mx4_linear_workspace_bytes,
     lora_block_norm, lora_sample,
+    lora_verify, lora_verify_workspace_bytes,
     KvCache, lora_kv_append, lora_kv_attention, lora_kv_attention_chunk, lora_kv_attention_workspace_bytes,
 )

@@ -39,6 +39,7 @@ EXPORTED = [
     "lora_mx4_quantize", "lora_mx4_dequantize", "lora_mx4_linear_workspace_bytes", "lora_mx4_linear",
     "lora_mx4_linear_q", "lora_block_norm", "lora_sample",
     "lora_kv_append", "lora_kv_attention_chunk", "lora_kv_attention_workspace_bytes", "lora_kv_attention",
+    "lora_verify_workspace_bytes", "lora_verify",
 ]
 
 
@@ -116,6 +117,8 @@ def lib():
         L.lora_shrink_expand_counted.restype = ctypes.c_int
         L.lora_shrink_expand_counted.argtypes = [_vp, _i64, _vp, _i64, _vp, _i64, _vp, _i64, _vp, _i64, _i64, _i64,
                                                  _i32, _i64, _i32, _f32, _f32, _vp, _sz, _vp, _sz, _vp]
+        L.lora_verify_workspace_bytes.restype = _sz
+        L.lora_verify_workspace_bytes.argtypes = [_i64, _i64]
         L.lora_kv_attention_chunk.restype = _i64
         L.lora_kv_attention_chunk.argtypes = [_i64, _i32, _i32, _i64]
         L.lora_kv_attention_workspace_bytes.restype = _sz
@@ -587,7 +590,7 @@ def _native():
         L = lib()
         m.bind(*(ctypes.cast(getattr(L, name), _vp).value for name in (
             "lora_mx4_quantize", "lora_mx4_dequantize", "lora_mx4_linear", "lora_mx4_linear_q", "lora_block_norm",
-            "lora_sample", "lora_kv_append", "lora_kv_attention")))
+            "lora_sample", "lora_kv_append", "lora_kv_attention", "lora_verify")))
         # the current stream's address without building a Stream object
         _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
             lambda device: torch.cuda.current_stream(device).cuda_stream)
@@ -663,6 +666,24 @@ def lora_sample(logits, u, tokens, temperature=None, top_k=None, top_p=None, min
                                               _stream_address(stream, logits))
     if st:
         raise LoraError(st, "lora_sample")
+    return tokens
+
+
+def lora_verify_workspace_bytes(B: int, n: int) -> int:
+    return int(lib().lora_verify_workspace_bytes(B, n))
+
+
+def lora_verify(target_logits, drafted, u, tokens, accepted, workspace, draft_logits=None, temperature=None, top_k=None,
+                top_p=None, min_p=None, logprobs=None, stream=None):
+    """Accepts drafted tokens ([B, n] int32, -1 behind the last of a sequence) against the target's logits ([B (n + 1), V])
+    by the random numbers u [B, n + 1], and draws the token behind them: tokens [B, n + 1] (then -1), accepted [B],
+    logprobs [B, n + 1].  draft_logits [B n, V]: what the drafts were drawn from under the same settings (vectors of B, as
+    for lora_sample); None: they came without probabilities.  workspace: tensor of lora_verify_workspace_bytes."""
+    st = (_native_module or _native()).verify(target_logits, draft_logits, drafted, u, temperature, top_k, top_p, min_p,
+                                              tokens, accepted, logprobs, workspace,
+                                              _stream_address(stream, target_logits))
+    if st:
+        raise LoraError(st, "lora_verify")
     return tokens
 
 

@@ -15,9 +15,9 @@ CSRC = os.path.join(HERE, "csrc")
 LIB = os.path.join(HERE, "liblora_det.so")
 BINDING = os.path.join(HERE, "_native.so")
 SOURCES = ["abi.hip", "shrink.hip", "expand.hip", "fused.hip", "streamed.hip", "sgmv_plan.hip",
-           "abi_step.hip", "mx4.hip", "mx4_linear.hip", "block_norm.hip", "sample.hip",
+           "abi_step.hip", "mx4.hip", "mx4_linear.hip", "block_norm.hip", "sample.hip", "verify.hip",
            "abi_kv.hip", "kv_append.hip", "kv_attention.hip"]
-HEADERS = ["device.h", "kernels.h", "shrink_tile.h", "step_kernels.h", "mx4.h", "mx4_tile.h", "kv_cache.h"]
+HEADERS = ["device.h", "kernels.h", "shrink_tile.h", "step_kernels.h", "mx4.h", "mx4_tile.h", "sample_row.h", "kv_cache.h"]
 
 HIPCC_FLAGS = [
     "--offload-arch=gfx950",

@@ -11,6 +11,7 @@ namespace {
 
 constexpr int64_t kMaxDim = (int64_t{1} << 31) - 1;
 constexpr int64_t kMaxGrid = (int64_t{1} << 31) - 1;
+constexpr int64_t kMaxThreads = (int64_t{1} << 32) - 1;    // of a launch
 constexpr int64_t kMaxGridY = 65535;
 constexpr int64_t kMaxColumns = int64_t{1} << 25;      // of a product
 constexpr int64_t kMaxTiles = int64_t{1} << 22;        // 64 x 128 tiles of a product's y
@@ -270,6 +271,61 @@ int lora_sample(const void* logits, int32_t logits_type, int64_t ld, int64_t B, 
     p.V = (int32_t)V;
     p.B = B;
     return launch_status(launch_sample(p, bf16, static_cast<hipStream_t>(stream)));
+}
+
+size_t lora_verify_workspace_bytes(int64_t B, int64_t n)
+{
+    if (B < 1 || n < 0 || n > kMaxDrafts || B > kMaxDraws / (2 * n + 1))
+        return 0;
+    return (size_t)verify_workspace(B, n);
+}
+
+int lora_verify(const void* target_logits, int64_t ld_target, const void* draft_logits, int64_t ld_draft,
+                int32_t logits_type, int64_t B, int64_t n, int64_t V, const int32_t* drafted, const float* u,
+                const float* temperature, const int32_t* top_k, const float* top_p, const float* min_p,
+                int32_t* tokens, int32_t* accepted, float* logprobs, void* workspace, size_t workspace_bytes,
+                void* stream)
+{
+    if (B < 0 || n < 0 || V < 1)
+        return LORA_ERR_SHAPE;
+    if (V > kMaxVocabulary || n > kMaxDrafts || (logits_type != LORA_LOGITS_BF16 && logits_type != LORA_LOGITS_F32))
+        return LORA_ERR_UNSUPPORTED;
+    if (B > kMaxDraws / (2 * n + 1) || verify_threads(B, n, V) > kMaxThreads)
+        return LORA_ERR_SHAPE;
+    if (B == 0)
+        return LORA_OK;
+    if (!target_logits || !u || !tokens || !accepted || !workspace || (n && !drafted))
+        return LORA_ERR_NULL;
+    if (ld_target < V || (draft_logits && n && ld_draft < V))
+        return LORA_ERR_SHAPE;
+    const bool bf16 = logits_type == LORA_LOGITS_BF16;
+    const void* ptrs[] = {drafted, u, temperature, top_k, top_p, min_p, tokens, accepted, logprobs};
+    for (const void* q : ptrs)
+        if (!aligned(q, 4))
+            return LORA_ERR_ALIGN;
+    if (!aligned(target_logits, bf16 ? 2 : 4) || !aligned(draft_logits, bf16 ? 2 : 4) || !aligned(workspace, 16))
+        return LORA_ERR_ALIGN;
+    if (workspace_bytes < (size_t)verify_workspace(B, n))
+        return LORA_ERR_WORKSPACE;
+    VerifyParams p{};
+    p.target = target_logits;
+    p.draft = n ? draft_logits : nullptr;
+    p.ld_t = ld_target;
+    p.ld_d = ld_draft;
+    p.drafted = drafted;
+    p.u = u;
+    p.temperature = temperature;
+    p.top_k = top_k;
+    p.top_p = top_p;
+    p.min_p = min_p;
+    p.tokens = tokens;
+    p.accepted = accepted;
+    p.logprobs = logprobs;
+    p.workspace = workspace;
+    p.V = (int32_t)V;
+    p.n = (int32_t)n;
+    p.B = B;
+    return launch_status(launch_verify(p, bf16, static_cast<hipStream_t>(stream)));
 }
 
 #pragma GCC visibility pop

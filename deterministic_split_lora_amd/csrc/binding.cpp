@@ -21,6 +21,7 @@ decltype(&lora_mx4_linear) linear_fn;
 decltype(&lora_mx4_linear_q) linear_q_fn;
 decltype(&lora_block_norm) norm_fn;
 decltype(&lora_sample) sample_fn;
+decltype(&lora_verify) verify_fn;
 decltype(&lora_kv_append) kv_append_fn;
 decltype(&lora_kv_attention) kv_attention_fn;
 
@@ -204,7 +205,7 @@ PyObject* linear(PyObject*, PyObject* const* a, Py_ssize_t n)
 // xq, xs, wq, ws, y, split_k, workspace, stream
 PyObject* linear_q(PyObject*, PyObject* const* a, Py_ssize_t n)
 {
-    return call(n, 8, [&] {
+    return call(n, 9, [&] {
         const Matrix y = matrix(a[4], kBf16, "y");
         const int64_t K = 2 * matrix(a[0], at::kByte, "x").cols;
         const Mx4 x = mx4(a[0], a[1], K, "x"), w = mx4(a[2], a[3], K, "W");
@@ -267,6 +268,61 @@ PyObject* sample(PyObject*, PyObject* const* a, Py_ssize_t n)
                          f32(vector(a[3], B, at::kFloat, "top_p")), f32(vector(a[4], B, at::kFloat, "min_p")),
                          f32(vector(a[5], B, at::kFloat, "u", false)), i32(vector(a[6], B, at::kInt, "tokens", false)),
                          f32(vector(a[7], B, at::kFloat, "logprobs")), address(a[8]));
+    });
+}
+
+// Logits of either type; `type` is the one they have to have, or None yet.
+Matrix logits(PyObject* arg, at::ScalarType* type, const char* name)
+{
+    if (!THPVariable_Check(arg))
+        refuse(PyExc_TypeError, "%s must be a tensor", name);
+    const at::ScalarType t = THPVariable_Unpack(arg).scalar_type();
+    if (t != kBf16 && t != at::kFloat)
+        refuse(PyExc_TypeError, "%s must be bfloat16 or float32, got %s", name, c10::toString(t));
+    if (*type == at::ScalarType::Undefined)
+        *type = t;
+    return matrix(arg, *type, name);
+}
+
+// A contiguous table [rows, cols].
+void* table(PyObject* arg, int64_t rows, int64_t cols, at::ScalarType type, const char* name, bool optional = false)
+{
+    const at::Tensor* t = tensor(arg, type, name, optional);
+    if (!t)
+        return nullptr;
+    if (t->dim() != 2 || t->size(0) != rows || t->size(1) != cols || !t->is_contiguous())
+        refuse(PyExc_ValueError, "%s must be contiguous [%lld, %lld]", name, (long long)rows, (long long)cols);
+    return t->data_ptr();
+}
+
+// target_logits, draft_logits, drafted, u, temperature, top_k, top_p, min_p, tokens, accepted,
+// logprobs, workspace, stream
+PyObject* verify(PyObject*, PyObject* const* a, Py_ssize_t count)
+{
+    return call(count, 13, [&] {
+        const at::Tensor* drafted = tensor(a[2], at::kInt, "drafted");
+        if (drafted->dim() != 2)
+            refuse(PyExc_ValueError, "drafted must be [sequences, drafts]");
+        const int64_t B = drafted->size(0), n = drafted->size(1);
+        at::ScalarType type = at::ScalarType::Undefined;
+        const Matrix target = logits(a[0], &type, "target_logits");
+        same_rows(B * (n + 1), target, "target_logits");
+        Matrix draft;
+        if (a[1] != Py_None) {
+            draft = logits(a[1], &type, "draft_logits");
+            same_rows(B * n, draft, "draft_logits");
+            if (draft.cols != target.cols)
+                refuse(PyExc_ValueError, "draft_logits must have %lld columns", (long long)target.cols);
+        }
+        const Workspace w = workspace(a[11]);
+        return verify_fn(target.p, target.ld, draft.p, draft.ld, type == kBf16 ? LORA_LOGITS_BF16 : LORA_LOGITS_F32, B,
+                         n, target.cols, i32(table(a[2], B, n, at::kInt, "drafted")),
+                         f32(table(a[3], B, n + 1, at::kFloat, "u")), f32(vector(a[4], B, at::kFloat, "temperature")),
+                         i32(vector(a[5], B, at::kInt, "top_k")), f32(vector(a[6], B, at::kFloat, "top_p")),
+                         f32(vector(a[7], B, at::kFloat, "min_p")),
+                         i32(table(a[8], B, n + 1, at::kInt, "tokens")),
+                         i32(vector(a[9], B, at::kInt, "accepted", false)),
+                         f32(table(a[10], B, n + 1, at::kFloat, "logprobs", true)), w.p, w.bytes, address(a[12]));
     });
 }
 
@@ -405,7 +461,7 @@ PyObject* kv_attention(PyObject*, PyObject* const* a, Py_ssize_t n)
 // The addresses of the entry points, in the order above.
 PyObject* bind(PyObject*, PyObject* const* a, Py_ssize_t n)
 {
-    return call(n, 8, [&] {
+    return call(n, 9, [&] {
         quantize_fn = reinterpret_cast<decltype(quantize_fn)>(address(a[0]));
         dequantize_fn = reinterpret_cast<decltype(dequantize_fn)>(address(a[1]));
         linear_fn = reinterpret_cast<decltype(linear_fn)>(address(a[2]));
@@ -414,6 +470,7 @@ PyObject* bind(PyObject*, PyObject* const* a, Py_ssize_t n)
         sample_fn = reinterpret_cast<decltype(sample_fn)>(address(a[5]));
         kv_append_fn = reinterpret_cast<decltype(kv_append_fn)>(address(a[6]));
         kv_attention_fn = reinterpret_cast<decltype(kv_attention_fn)>(address(a[7]));
+        verify_fn = reinterpret_cast<decltype(verify_fn)>(address(a[8]));
         return 0;
     });
 }
@@ -432,6 +489,7 @@ PyMethodDef methods[] = {
     {"mx4_linear_q", fast(linear_q), METH_FASTCALL, nullptr},
     {"block_norm", fast(block_norm), METH_FASTCALL, nullptr},
     {"sample", fast(sample), METH_FASTCALL, nullptr},
+    {"verify", fast(verify), METH_FASTCALL, nullptr},
     {"kv_append", fast(kv_append), METH_FASTCALL, nullptr},
     {"kv_attention", fast(kv_attention), METH_FASTCALL, nullptr},
     {nullptr, nullptr, 0, nullptr}};

@@ -91,6 +91,33 @@ struct SampleParams {
 
 hipError_t launch_sample(const SampleParams& p, bool bf16, hipStream_t st);
 
+struct VerifyParams {
+    const void* target;             // [B * (n + 1)][ld_t]
+    const void* draft;              // [B * n][ld_d], may be null: drafts of certainty
+    int64_t ld_t;
+    int64_t ld_d;
+    const int32_t* drafted;         // [B][n]
+    const float* u;                 // [B][n + 1]
+    const float* temperature;       // each may be null: 1, off, off, off
+    const int32_t* top_k;
+    const float* top_p;
+    const float* min_p;
+    int32_t* tokens;                // [B][n + 1]
+    int32_t* accepted;              // [B]
+    float* logprobs;                // [B][n + 1], may be null
+    void* workspace;
+    int32_t V;
+    int32_t n;
+    int64_t B;
+};
+
+constexpr int kMaxDrafts = 63;               // of a sequence: a lane each, and one for the row behind them
+
+// Bytes of workspace, and threads of the largest launch.
+int64_t verify_workspace(int64_t B, int64_t n);
+int64_t verify_threads(int64_t B, int64_t n, int64_t V);
+hipError_t launch_verify(const VerifyParams& p, bool bf16, hipStream_t st);
+
 constexpr int kKvBlock = 16;                 // tokens that share a scale in the cache
 
 // The paged cache and the batch's tables (kv_cache.h has the layouts).

@@ -632,6 +632,44 @@ int lora_sample(const void* logits, int32_t logits_type, int64_t ld, int64_t B, 
                 const int32_t* top_k, const float* top_p, const float* min_p, const float* u, int32_t* tokens,
                 float* logprobs, void* stream);
 
+/*
+ * Verifies drafted tokens against the target's distributions and draws the token
+ * that follows the accepted ones, so that what comes out is distributed as the
+ * target's own tokens.  Sequence i has n drafted tokens x_0 .. x_{n-1}; row
+ * i (n + 1) + j of target_logits is the target's row for the place of x_j (j = n:
+ * behind them all), row i n + j of draft_logits the row that x_j was drawn from.
+ * With w_j the kept weights of a row as lora_sample defines them under the
+ * sequence's settings, W_j their sum:
+ *     P_j(y) = rint(w_j(y) (2^40 / W_j)),  in fp64; 0 where W_j is 0
+ *     Q_j    the same of the draft's row and the same settings;
+ *            draft_logits NULL: 2^40 at x_j, 0 elsewhere (a draft of certainty)
+ * x_j is accepted, one after another from j = 0, while  u[i][j] Q_j(x_j) < P_j(x_j)
+ * (a product in fp64; u <= 0 or NaN: 0).  A number outside [0, V) as x_j ends the
+ * drafts (a sequence with fewer).  Let a be the number accepted.  The token behind
+ * them is drawn with u[i][n]:
+ *     where x_a was not accepted, from max(P_a - Q_a, 0) (from w_a, if that is 0
+ *     everywhere); where the drafts ended, from w_a, as lora_sample draws:
+ *     with S the sum of these numbers, the lowest index whose sum of the numbers up
+ *     to it exceeds t = floor(u S) (at most S - 1)
+ * Greedy rows (temperature <= 0 or NaN) have weight 1 at their first token.  A row of
+ * -inf only gives the token -1.
+ *   tokens    int32 [B][n + 1]: the accepted ones, the drawn one, then -1
+ *   accepted  int32 [B]: a
+ *   logprobs  fp32 [B][n + 1] or NULL: log(w_j(token) / W_j), -inf for -1
+ * logits, settings and their defaults as for lora_sample (rows of both tensors have
+ * the same type; settings are per sequence, [B]); drafted int32 [B][n], u fp32
+ * [B][n + 1].  0 <= n <= 63, B (2n + 1) <= 2^21, B V < 2^35.
+ * workspace: lora_verify_workspace_bytes(B, n) bytes, 16-byte aligned, no
+ * initialisation needed.  Three launches.
+ */
+size_t lora_verify_workspace_bytes(int64_t B, int64_t n);
+
+int lora_verify(const void* target_logits, int64_t ld_target, const void* draft_logits, int64_t ld_draft,
+                int32_t logits_type, int64_t B, int64_t n, int64_t V, const int32_t* drafted, const float* u,
+                const float* temperature, const int32_t* top_k, const float* top_p, const float* min_p,
+                int32_t* tokens, int32_t* accepted, float* logprobs, void* workspace, size_t workspace_bytes,
+                void* stream);
+
 /* ---------------------------------------------------------------------------
  * The paged key / value cache in 8 bits, and attention over it.
  *
