@@ -120,7 +120,7 @@ def lib():
         L.lora_verify_workspace_bytes.restype = _sz
         L.lora_verify_workspace_bytes.argtypes = [_i64, _i64]
         L.lora_kv_attention_chunk.restype = _i64
-        L.lora_kv_attention_chunk.argtypes = [_i64, _i32, _i32, _i64]
+        L.lora_kv_attention_chunk.argtypes = [_i64, _i32, _i32, _i32, _i64]
         L.lora_kv_attention_workspace_bytes.restype = _sz
         L.lora_kv_attention_workspace_bytes.argtypes = [_i64, _i32, _i32, _i32, _i64, _i64, _i64]
         L.lora_shrink_counter_bytes.restype = _sz
@@ -710,9 +710,9 @@ def lora_kv_append(k, v, cache, q=None, q_out=None, q_norm=None, k_norm=None, ro
     return q_out
 
 
-def lora_kv_attention_chunk(max_new: int, q_heads: int, heads: int, max_len: int) -> int:
+def lora_kv_attention_chunk(max_new: int, q_heads: int, heads: int, head_dim: int, max_len: int) -> int:
     """The chunk that lora_kv_attention takes for 0 (0 for invalid sizes)."""
-    return int(lib().lora_kv_attention_chunk(max_new, q_heads, heads, max_len))
+    return int(lib().lora_kv_attention_chunk(max_new, q_heads, heads, head_dim, max_len))
 
 
 def lora_kv_attention_workspace_bytes(T: int, q_heads: int, heads: int, head_dim: int, max_new: int, max_len: int,

@@ -163,11 +163,11 @@ int lora_kv_append(const lora_kv_cache* cache, const uint16_t* q, int64_t ld_q, 
     return launch_status(launch_kv_append(p, static_cast<hipStream_t>(stream)));
 }
 
-int64_t lora_kv_attention_chunk(int64_t max_new, int32_t q_heads, int32_t heads, int64_t max_len)
+int64_t lora_kv_attention_chunk(int64_t max_new, int32_t q_heads, int32_t heads, int32_t head_dim, int64_t max_len)
 {
-    if (check_attention_sizes(0, q_heads, heads, 64, max_new, max_len, 0) != LORA_OK)
+    if (check_attention_sizes(0, q_heads, heads, head_dim, max_new, max_len, 0) != LORA_OK)
         return 0;
-    return kv_attention_chunk(max_new, q_heads, heads, max_len);
+    return kv_attention_chunk(max_new, q_heads, heads, head_dim, max_len);
 }
 
 size_t lora_kv_attention_workspace_bytes(int64_t T, int32_t q_heads, int32_t heads, int32_t head_dim, int64_t max_new,
@@ -176,7 +176,7 @@ size_t lora_kv_attention_workspace_bytes(int64_t T, int32_t q_heads, int32_t hea
     if (check_attention_sizes(T, q_heads, heads, head_dim, max_new, max_len, chunk) != LORA_OK || T == 0)
         return 0;
     if (chunk == 0)
-        chunk = kv_attention_chunk(max_new, q_heads, heads, max_len);
+        chunk = kv_attention_chunk(max_new, q_heads, heads, head_dim, max_len);
     if (max_len <= chunk)
         return 0;
     if (join_threads(T, q_heads, head_dim) > kMaxThreads || T * q_heads * ((max_len + chunk - 1) / chunk) > kMaxThreads)
@@ -211,10 +211,10 @@ int lora_kv_attention(const lora_kv_cache* cache, const uint16_t* q, int64_t ld_
     if (!aligned(q, 16) || !aligned(out, 16) || !aligned(lse, 4) || !aligned(workspace, 16) || ld_q % 8 || ld_out % 8)
         return LORA_ERR_ALIGN;
     if (chunk == 0)                          // by the caller's max_len, as the workspace's size
-        chunk = kv_attention_chunk(max_new, q_heads, H, max_len);
+        chunk = kv_attention_chunk(max_new, q_heads, H, D, max_len);
     const int64_t capacity = cache->max_pages * cache->page_size;
     max_len = max_len < capacity ? max_len : capacity;
-    if (kv_attention_blocks(T, cache->n_seqs, max_new, q_heads, H, max_len, chunk) > kMaxThreads / kWaveGroup ||
+    if (kv_attention_blocks(T, cache->n_seqs, max_new, q_heads, H, D, max_len, chunk) > kMaxThreads / kWaveGroup ||
         (max_len > chunk && join_threads(T, q_heads, D) > kMaxThreads))
         return LORA_ERR_SHAPE;
     const int64_t need = kv_attention_workspace(T, q_heads, D, max_len, chunk);

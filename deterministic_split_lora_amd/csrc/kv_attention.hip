@@ -13,6 +13,7 @@
 #include "kv_cache.h"
 
 #include <math.h>
+#include <type_traits>
 
 namespace lora {
 
@@ -398,6 +399,344 @@ __global__ void __launch_bounds__(kWaves * 64) k_attention(KvAttentionParams p, 
     }
 }
 
+// ---------------------------------------------------------------------------
+// Many rows (prompts): bound by the matrix cores.  A workgroup has 128 rows, a wave
+// 32 of them; K and V of a step are widened to bf16 on their way to LDS, once for
+// all waves, and lie there in the order of the operands:
+//   S^T = K Q^T       32x32x16 products, 32 keys x 32 rows
+//   O^T += V^T P^T    32x32x16 products, 32 d x 32 rows
+// A lane half gets the S of keys 4h .. 4h+3 and 8 + 4h .. 8 + 4h+3 of each block of 16,
+// and V's tokens lie in that order, so P goes from one product to the other as it is.
+// While a wave takes the softmax of a step it multiplies the next one (S), which does
+// not depend on it.
+// ---------------------------------------------------------------------------
+typedef float f32x16 __attribute__((ext_vector_type(16)));
+
+constexpr int kTileRows = kWaves * 32;
+
+template <int D>
+struct TileLds {
+    u32x4 k[2][D / 16][2][kStep];            // bf16: 8 d of a key, for each lane half
+    u32x4 v[2][kStep / kKvBlock][2][D];      // bf16: 8 keys of a d, for each lane half
+    uint32_t nan_step[2];                    // the last step with a value that is NaN
+    uint16_t nan[2][kStep / kKvBlock][D];    // then: which keys' value of a d is
+};
+
+__device__ __forceinline__ float half_max(float v)
+{
+    const auto r = __builtin_amdgcn_permlane32_swap(__builtin_bit_cast(uint32_t, v), __builtin_bit_cast(uint32_t, v),
+                                                    false, false);
+    const uint32_t a = r[0], b = r[1];       // a bit cast takes a vector's first element
+    return fmaxf(__builtin_bit_cast(float, a), __builtin_bit_cast(float, b));
+}
+
+__device__ __forceinline__ float half_sum(float v)
+{
+    const auto r = __builtin_amdgcn_permlane32_swap(__builtin_bit_cast(uint32_t, v), __builtin_bit_cast(uint32_t, v),
+                                                    false, false);
+    const uint32_t a = r[0], b = r[1];
+    return __builtin_bit_cast(float, a) + __builtin_bit_cast(float, b);
+}
+
+template <int D>
+__global__ void __launch_bounds__(kWaves * 64, D == 256 ? 1 : 2) k_attention_tile(KvAttentionParams p, uint32_t slots)
+{
+    constexpr int kKeys = kStep;
+    constexpr int kTiles = kKeys / 32;       // tiles of 32 keys
+    constexpr int kBlocks = kKeys / kKvBlock;
+    constexpr int kDeep = D / 16;            // products of 16 d
+    constexpr int kOut = D / 32;             // tiles of 32 d
+    constexpr int kPieces = D / 64;          // 16-byte pieces of K, and of V, a thread brings to LDS
+    __shared__ __align__(16) TileLds<D> lds;
+    const int H = p.cache.heads, G = p.q_heads / H;
+    const int lane = threadIdx.x & 63, r = lane & 31, h = lane >> 5;
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int head = (int)(blockIdx.x % (uint32_t)H);
+    const uint32_t tile = blockIdx.x / (uint32_t)H;
+    // a prompt's last rows see the most keys: they begin first
+    const int64_t slot = slots - 1 - tile % slots, chunk = tile / slots;
+
+    const Work w = find_work<kTileRows>(p, slot, G);
+    if (w.rows == 0)
+        return;
+    const int first_token = (int)w.row0 / G, last_token = ((int)w.row0 + w.rows - 1) / G;
+    const Seen first = seen_by(p, w.s, first_token), last = seen_by(p, w.s, last_token);
+    const int64_t begin = max(chunk * p.chunk, (int64_t)first.lo / kKeys * kKeys);
+    const int64_t end = min((chunk + 1) * p.chunk, (int64_t)last.hi + 1);
+    const bool several = p.partial != nullptr;
+    if (several && begin >= end)
+        return;
+
+    const int row = wave * 32 + r;
+    const bool in = row < w.rows;
+    const int at = (int)w.row0 + (in ? row : 0), token = at / G, q_head = head * G + at - token * G;
+    Seen seen = seen_by(p, w.s, token);
+    if (!in)
+        seen.hi = -1;
+    bf16x8 q[kDeep];
+    {
+        const uint16_t* src = p.q + (w.s.first + token) * p.ld_q + (int64_t)q_head * D + 8 * h;
+#pragma unroll
+        for (int j = 0; j < kDeep; ++j)
+            q[j] = load_bf16x8(src + 16 * j);
+    }
+
+    f32x16 o[kOut];
+#pragma unroll
+    for (int d = 0; d < kOut; ++d)
+        o[d] = f32x16{};
+    float m = -INFINITY, l = 0.0f;           // l: of this lane's keys
+    const float sl = p.scale * kLog2e;
+    const int P = p.cache.page_size;
+
+    // A wave brings its block of a step to LDS: a thread 16 d of a key, and the keys of a d.
+    static_assert(kBlocks == kWaves, "");
+    const int k_key = lane % kKvBlock, k_piece = lane / kKvBlock;
+    // the sequence's row of the table, read by scalar loads
+    typedef __attribute__((address_space(4))) const int32_t constant_i32;
+    constant_i32* pages = (constant_i32*)(p.cache.page_table + __builtin_amdgcn_readfirstlane((int)w.b) * p.cache.ld_table);
+    const int shift = p.cache.page_shift, n_pages = p.cache.n_pages;
+    const int max_page = (int)min(p.cache.max_pages, (int64_t)1 << 30);
+    auto page_of = [&](int key) {
+        const int i = key >> shift, page = pages[min(i, max_page - 1)];
+        return i < max_page && page >= 0 && page < n_pages ? page : -1;
+    };
+    // The page of this wave's block of a step; `gone`: the step's blocks without one, a bit each.
+    auto page_at = [&](int step, uint32_t& gone) {
+        const int page = page_of(step * kKeys + wave * kKvBlock);
+        gone = page < 0 ? 15u : 0u;
+        if (P < kKeys) {
+            gone = 0;
+#pragma unroll
+            for (int u = 0; u < kBlocks; ++u)
+                gone |= (page_of(step * kKeys + u * kKvBlock) < 0 ? 1u : 0u) << u;
+        }
+        return page;
+    };
+    // every row of the tile sees every key of most steps
+    auto whole = [&](int step) { return step * kKeys >= last.lo && step * kKeys + kKeys - 1 <= first.hi; };
+
+    u32x4 kr[kPieces], vr[kPieces];
+    uint32_t kscale, vscale;
+    auto load_k = [&](int step, int page) __attribute__((always_inline)) {
+        const int64_t g = max(page, 0);
+        const int at = head * P + ((step * kKeys + wave * kKvBlock) & (P - 1));    // in tokens of all heads
+        const uint8_t* src = p.cache.k + (g * p.cache.ld_k + (int64_t)at * D);
+#pragma unroll
+        for (int j = 0; j < kPieces; ++j)
+            kr[j] = *(const global_u32x4*)(src + (k_key * D + 16 * k_piece + 64 * j));
+        kscale = p.cache.k_scales[g * p.cache.ld_ks + at / kKvBlock];
+    };
+    auto load_v = [&](int step, int page) __attribute__((always_inline)) {
+        const int64_t g = max(page, 0);
+        const int at = head * P + ((step * kKeys + wave * kKvBlock) & (P - 1));
+        const uint8_t* src = p.cache.v + (g * p.cache.ld_v + (int64_t)at * D);
+#pragma unroll
+        for (int j = 0; j < kPieces; ++j)
+            vr[j] = *(const global_u32x4*)(src + (lane * 16 + 1024 * j));
+        vscale = p.cache.v_scales[g * p.cache.ld_vs + at / kKvBlock];
+    };
+    auto store_k = [&](int buf) __attribute__((always_inline)) {
+        const float s = pow2_of_scale(kscale);
+#pragma unroll
+        for (int j = 0; j < kPieces; ++j) {
+            lds.k[buf][k_piece + 4 * j][0][wave * kKvBlock + k_key] = __builtin_bit_cast(u32x4, widen(kr[j][0], kr[j][1], s));
+            lds.k[buf][k_piece + 4 * j][1][wave * kKvBlock + k_key] = __builtin_bit_cast(u32x4, widen(kr[j][2], kr[j][3], s));
+        }
+    };
+    // gaps: some rows do not see all keys of the step
+    auto store_v = [&](bool gaps, int buf, int step, int page) __attribute__((always_inline)) {
+        if (gaps) {
+            // a block that was never written may hold anything, its scale too
+            const bool unseen = page < 0 || step * kKeys + wave * kKvBlock > last.hi;
+            vscale = unseen ? 127u : vscale;
+#pragma unroll
+            for (int j = 0; j < kPieces; ++j) {
+                uint32_t bad = 0;
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const uint32_t c = unseen ? 0u : vr[j][i], b = nan_bytes(c) >> 7;
+                    vr[j][i] = c & ~(b * 0xFFu);
+                    bad |= ((b | b >> 7 | b >> 14 | b >> 21) & 15u) << (4 * i);
+                }
+                lds.nan[buf][wave][lane + 64 * j] = (uint16_t)bad;
+                if (bad)
+                    lds.nan_step[buf] = (uint32_t)step;
+            }
+        }
+        const float s = pow2_of_scale(vscale);
+#pragma unroll
+        for (int j = 0; j < kPieces; ++j) {
+            lds.v[buf][wave][0][lane + 64 * j] = __builtin_bit_cast(u32x4, widen(vr[j][0], vr[j][2], s));
+            lds.v[buf][wave][1][lane + 64 * j] = __builtin_bit_cast(u32x4, widen(vr[j][1], vr[j][3], s));
+        }
+    };
+
+    typedef f32x16 Logits[kTiles];
+    typedef bf16x8 Probs[kBlocks];
+    auto product = [&](int buf, Logits& out) __attribute__((always_inline)) {
+#pragma unroll
+        for (int t = 0; t < kTiles; ++t)
+            out[t] = f32x16{};
+#pragma unroll
+        for (int j = 0; j < kDeep; ++j)
+#pragma unroll
+            for (int t = 0; t < kTiles; ++t) {
+                const bf16x8 k = __builtin_bit_cast(bf16x8, lds.k[buf][j][h][32 * t + r]);
+                out[t] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(k, q[j], out[t], 0, 0, 0);
+            }
+    };
+    auto output = [&](int buf, const Probs& prob) __attribute__((always_inline)) {
+#pragma unroll
+        for (int u = 0; u < kBlocks; ++u)
+#pragma unroll
+            for (int d = 0; d < kOut; ++d) {
+                const bf16x8 v = __builtin_bit_cast(bf16x8, lds.v[buf][u][h][32 * d + r]);
+                o[d] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(v, prob[u], o[d], 0, 0, 0);
+            }
+    };
+    // a value that is NaN reaches the rows that see its key, and no others
+    auto spread_nan = [&](int buf, int step) __attribute__((always_inline)) {
+        const int from = min(max(seen.lo - step * kKeys, 0), kKeys), to = min(max(seen.hi + 1 - step * kKeys, 0), kKeys);
+        const uint64_t sees =
+            (to < 64 ? (uint64_t(1) << to) - 1 : ~uint64_t(0)) & (from < 64 ? ~uint64_t(0) << from : 0);
+#pragma unroll
+        for (int d = 0; d < kOut; ++d)
+#pragma unroll
+            for (int i = 0; i < 16; ++i) {
+                uint64_t bad = 0;
+#pragma unroll
+                for (int u = 0; u < kBlocks; ++u)
+                    bad |= (uint64_t)lds.nan[buf][u][32 * d + 8 * (i / 4) + 4 * h + i % 4] << (16 * u);
+                o[d][i] = bad & sees ? __builtin_nanf("") : o[d][i];
+            }
+    };
+
+    const int s0 = (int)(begin / kKeys), s1 = (int)((end + kKeys - 1) / kKeys);
+    int page_v = -1, page_k = -1;            // of the next step, the one behind it
+    uint32_t gone = 0, gone_next = 0, gone_far = 0;    // of this step, the next, the one behind it
+    Logits s_even, s_odd;                    // of the even and odd steps from the first on
+    if (threadIdx.x < 2)
+        lds.nan_step[threadIdx.x] = 0xFFFFFFFFu;
+    if (s0 < s1) {
+        const int page = page_at(s0, gone);
+        page_v = page_at(s0 + 1, gone_next);
+        page_k = page_at(s0 + 2, gone_far);
+        load_k(s0, page);
+        load_v(s0, page);
+        store_k(s0 & 1);
+        load_k(s0 + 1, page_v);
+        __syncthreads();
+        store_v(!whole(s0) || gone, s0 & 1, s0, page);
+        store_k((s0 + 1) & 1);
+        load_v(s0 + 1, page_v);
+        load_k(s0 + 2, page_k);
+        __syncthreads();
+        product(s0 & 1, s_even);
+        __syncthreads();                     // K of the first step is read: its place is free
+    }
+    // One step: its S are in s, those of the next go to s_next.  V of the next step and K of the
+    // one behind it have been loaded during the step before.
+    auto take = [&](int step, Logits& s, Logits& s_next) __attribute__((always_inline)) {
+        const int buf = step & 1;
+        const bool gaps = !whole(step) || gone;
+        if (gaps) {
+            const int key0 = step * kKeys + 4 * h;
+#pragma unroll
+            for (int t = 0; t < kTiles; ++t)
+#pragma unroll
+                for (int i = 0; i < 16; ++i) {
+                    const int key = key0 + 32 * t + 8 * (i / 4) + i % 4;
+                    const bool sees = key >= seen.lo && key <= seen.hi && !(gone >> (2 * t + i / 8) & 1);
+                    s[t][i] = sees ? s[t][i] : -INFINITY;
+                }
+        }
+        float top = -INFINITY;
+#pragma unroll
+        for (int t = 0; t < kTiles; ++t)
+#pragma unroll
+            for (int i = 0; i < 16; ++i)
+                top = fmaxf(top, s[t][i]);
+        const float mn = fmaxf(m, half_max(top) * sl);
+        if (__any(mn > m)) {
+            const float f = __builtin_amdgcn_exp2f(m - shift_of(mn));
+            l *= f;
+            m = mn;
+#pragma unroll
+            for (int d = 0; d < kOut; ++d)
+#pragma unroll
+                for (int i = 0; i < 16; ++i)
+                    o[d][i] *= f;
+        }
+        const float shift = shift_of(m);
+        // a wave with products to give comes before the others' vector work: 820 -> 805 us
+        // for prompts of 8191 and 5119 tokens, 32 heads
+        __builtin_amdgcn_s_setprio(1);
+        product(buf ^ 1, s_next);
+        Probs prob;
+        float sum = 0.0f;                    // of the P before their rounding, which lse would show
+#pragma unroll
+        for (int t = 0; t < kTiles; ++t)
+#pragma unroll
+            for (int i = 0; i < 16; ++i) {
+                const float x = __builtin_amdgcn_exp2f(fmaf(s[t][i], sl, -shift));
+                sum += x;
+                prob[2 * t + i / 8][i % 8] = (__bf16)x;
+            }
+        l += sum;
+        store_k(buf);
+        output(buf, prob);
+        __builtin_amdgcn_s_setprio(0);
+        if (gaps && lds.nan_step[buf] == (uint32_t)step)
+            spread_nan(buf, step);
+        store_v(!whole(step + 1) || gone_next, buf ^ 1, step + 1, page_v);
+        page_v = page_k;
+        load_v(step + 2, page_v);
+        gone = gone_next;
+        gone_next = gone_far;
+        page_k = page_at(step + 3, gone_far);
+        load_k(step + 3, page_k);
+        __syncthreads();
+    };
+    // two steps a turn, so that nothing moves from the registers of a step to those of another
+#pragma unroll 1
+    for (int step = s0; step < s1; step += 2) {
+        take(step, s_even, s_odd);
+        if (step + 1 < s1)
+            take(step + 1, s_odd, s_even);
+    }
+    l = half_sum(l);
+    if (!in)
+        return;
+    typedef __bf16 bf16x4 __attribute__((ext_vector_type(4)));
+    const int64_t out_row = w.s.first + token;
+    if (several) {
+        float* dst = p.partial + ((chunk * p.T + out_row) * p.q_heads + q_head) * partial_floats(D);
+#pragma unroll
+        for (int d = 0; d < kOut; ++d)
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                *reinterpret_cast<f32x4*>(dst + 4 + 32 * d + 8 * i + 4 * h) =
+                    f32x4{o[d][4 * i], o[d][4 * i + 1], o[d][4 * i + 2], o[d][4 * i + 3]};
+        if (h == 0) {
+            dst[0] = m;
+            dst[1] = l;
+        }
+    } else {
+        const float inv = l == 0.0f ? 0.0f : 1.0f / l;
+        uint16_t* dst = p.out + out_row * p.ld_out + (int64_t)q_head * D;
+#pragma unroll
+        for (int d = 0; d < kOut; ++d)
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                *reinterpret_cast<bf16x4*>(dst + 32 * d + 8 * i + 4 * h) =
+                    bf16x4{(__bf16)(o[d][4 * i] * inv), (__bf16)(o[d][4 * i + 1] * inv), (__bf16)(o[d][4 * i + 2] * inv),
+                           (__bf16)(o[d][4 * i + 3] * inv)};
+        if (p.lse && h == 0)
+            p.lse[out_row * p.ld_lse + q_head] = l == 0.0f ? -INFINITY : (m + log2f(l)) * kLn2;
+    }
+}
+
 // Joins the chunks of each row in ascending order: D / 4 threads a row, a block for
 // heads of one token.
 template <int D>
@@ -443,10 +782,10 @@ __global__ void __launch_bounds__(256) k_join(KvAttentionParams p)
 }
 
 // Rows of a tile that these sizes get; up to 64 rows a sequence the waves split the keys.
-int tile_rows(int64_t max_new, int G)
+int tile_rows(int64_t max_new, int G, int D)
 {
     const int64_t rows = max_new * G;
-    return rows <= 16 ? 16 : rows <= 64 ? 32 : 128;
+    return rows <= 16 ? 16 : rows <= 64 ? 32 : kTileRows;
 }
 
 int64_t tile_slots(int64_t T, int64_t n_seqs, int R, int G)
@@ -457,7 +796,7 @@ int64_t tile_slots(int64_t T, int64_t n_seqs, int R, int G)
 template <int D>
 hipError_t launch(const KvAttentionParams& p, hipStream_t st)
 {
-    const int G = p.q_heads / p.cache.heads, R = tile_rows(p.max_new, G);
+    const int G = p.q_heads / p.cache.heads, R = tile_rows(p.max_new, G, D);
     const int64_t slots = tile_slots(p.T, p.cache.n_seqs, R, G);
     const int64_t chunks = (p.max_len + p.chunk - 1) / p.chunk;
     const dim3 grid((unsigned)(slots * p.cache.heads * chunks)), threads(kWaves * 64);
@@ -466,7 +805,7 @@ hipError_t launch(const KvAttentionParams& p, hipStream_t st)
     else if (R == 32)
         hipLaunchKernelGGL((k_attention<D, 2, true>), grid, threads, 0, st, p, (uint32_t)slots);
     else
-        hipLaunchKernelGGL((k_attention<D, 2, false>), grid, threads, 0, st, p, (uint32_t)slots);
+        hipLaunchKernelGGL(k_attention_tile<D>, grid, threads, 0, st, p, (uint32_t)slots);
     if (p.partial) {
         const int per = 256 / (D / 4);
         hipLaunchKernelGGL(k_join<D>, dim3((unsigned)(p.T * ((p.q_heads + per - 1) / per))), dim3(256), 0, st, p);
@@ -476,9 +815,9 @@ hipError_t launch(const KvAttentionParams& p, hipStream_t st)
 
 }  // namespace
 
-int64_t kv_attention_chunk(int64_t max_new, int32_t q_heads, int32_t kv_heads, int64_t max_len)
+int64_t kv_attention_chunk(int64_t max_new, int32_t q_heads, int32_t kv_heads, int32_t D, int64_t max_len)
 {
-    const int G = q_heads / kv_heads, R = tile_rows(max_new, G);
+    const int G = q_heads / kv_heads, R = tile_rows(max_new, G, D);
     const int64_t tiles = (max_new * G + R - 1) / R * kv_heads;
     const int64_t splits = tiles < 512 ? 512 / tiles : 1;
     const int64_t chunk = (max_len + splits - 1) / splits;
@@ -491,11 +830,11 @@ int64_t kv_attention_workspace(int64_t T, int32_t q_heads, int32_t D, int64_t ma
     return chunks > 1 ? chunks * T * q_heads * partial_floats(D) * 4 : 0;
 }
 
-int64_t kv_attention_blocks(int64_t T, int64_t n_seqs, int64_t max_new, int32_t q_heads, int32_t kv_heads,
+int64_t kv_attention_blocks(int64_t T, int64_t n_seqs, int64_t max_new, int32_t q_heads, int32_t kv_heads, int32_t D,
                             int64_t max_len, int64_t chunk)
 {
     const int G = q_heads / kv_heads;
-    return tile_slots(T, n_seqs, tile_rows(max_new, G), G) * kv_heads * ((max_len + chunk - 1) / chunk);
+    return tile_slots(T, n_seqs, tile_rows(max_new, G, D), G) * kv_heads * ((max_len + chunk - 1) / chunk);
 }
 
 hipError_t launch_kv_attention(const KvAttentionParams& p, hipStream_t st)

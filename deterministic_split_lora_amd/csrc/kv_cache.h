@@ -53,12 +53,15 @@ __device__ __forceinline__ int64_t kv_find(const KvCacheView& c, int64_t w, F at
     return b;
 }
 
-// The page that holds a sequence's tokens [p, p + kKvBlock), or -1 if there is none.
+// The page that holds a sequence's tokens [p, p + kKvBlock), or -1 if there is none;
+// p is not negative.  The table is read through the constant address space: a scalar
+// load where p is the same in the whole wave.
 __device__ __forceinline__ int32_t kv_page(const KvCacheView& c, int64_t b, int64_t p)
 {
+    typedef __attribute__((address_space(4))) const int32_t constant_i32;
     const int64_t i = p >> c.page_shift;
-    const int32_t page = i < c.max_pages ? c.page_table[b * c.ld_table + i] : -1;
-    return page >= 0 && page < c.n_pages ? page : -1;
+    const int32_t page = *(constant_i32*)(c.page_table + b * c.ld_table + min(i, c.max_pages - 1));
+    return i < c.max_pages && page >= 0 && page < c.n_pages ? page : -1;
 }
 
 }  // namespace lora

@@ -190,10 +190,10 @@ struct KvAttentionParams {
 constexpr int kKvChunkUnit = 256;
 
 // The chunk that these sizes get by default.
-int64_t kv_attention_chunk(int64_t max_new, int32_t q_heads, int32_t kv_heads, int64_t max_len);
+int64_t kv_attention_chunk(int64_t max_new, int32_t q_heads, int32_t kv_heads, int32_t D, int64_t max_len);
 // Bytes of workspace (0: one chunk) and blocks of a launch with these sizes.
 int64_t kv_attention_workspace(int64_t T, int32_t q_heads, int32_t D, int64_t max_len, int64_t chunk);
-int64_t kv_attention_blocks(int64_t T, int64_t n_seqs, int64_t max_new, int32_t q_heads, int32_t kv_heads,
+int64_t kv_attention_blocks(int64_t T, int64_t n_seqs, int64_t max_new, int32_t q_heads, int32_t kv_heads, int32_t D,
                             int64_t max_len, int64_t chunk);
 hipError_t launch_kv_attention(const KvAttentionParams& p, hipStream_t st);
 

@@ -782,7 +782,7 @@ int lora_kv_append(const lora_kv_cache* cache, const uint16_t* q, int64_t ld_q, 
  * initialisation needed (NULL where that is 0; 0 is also returned for invalid input).
  * One launch, two with more than one chunk.
  */
-int64_t lora_kv_attention_chunk(int64_t max_new, int32_t q_heads, int32_t heads, int64_t max_len);
+int64_t lora_kv_attention_chunk(int64_t max_new, int32_t q_heads, int32_t heads, int32_t head_dim, int64_t max_len);
 size_t lora_kv_attention_workspace_bytes(int64_t T, int32_t q_heads, int32_t heads, int32_t head_dim, int64_t max_new,
                                          int64_t max_len, int64_t chunk);
 

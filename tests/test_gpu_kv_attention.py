@@ -166,7 +166,7 @@ def test_chunks_by_the_rule():
     q, qg = heads_bf16(1, 4, 64, 1.0, 4, "q")
     g = batch.gpu()
     n = g.page_table.shape[1] * 64
-    chunk = dsl.lora_kv_attention_chunk(1, 4, 1, n)
+    chunk = dsl.lora_kv_attention_chunk(1, 4, 1, 64, n)
     assert chunk % 256 == 0 and 0 < chunk < n
     assert t.equal(attend(qg, g, 1)[0], attend(qg, g, 1, chunk=chunk)[0])
 

@@ -155,10 +155,10 @@ def test_attention_workspace():
 
 def test_attention_chunk_rule():
     rule = dsl.lora_kv_attention_chunk
-    assert rule(0, 8, 2, 100) == 0 and rule(1, 7, 2, 100) == 0 and rule(1, 8, 2, 0) == 0
+    assert rule(0, 8, 2, 128, 100) == 0 and rule(1, 7, 2, 128, 100) == 0 and rule(1, 8, 2, 128, 0) == 0 and rule(1, 8, 2, 96, 9) == 0
     for max_new, Hq, H, n in [(1, 32, 8, 100), (1, 32, 8, 131072), (5, 32, 8, 6000), (512, 32, 8, 32768), (8192, 64, 8, 8192),
                               (1, 8, 1, 1 << 30), (1 << 20, 8, 8, 1 << 20)]:
-        c = rule(max_new, Hq, H, n)
+        c = rule(max_new, Hq, H, 128, n)
         assert c > 0 and c % 256 == 0
 
 
