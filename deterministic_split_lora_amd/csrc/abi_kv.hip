@@ -84,12 +84,6 @@ KvCacheView view(const lora_kv_cache* c)
     return v;
 }
 
-// Threads of the pass that joins several chunks: blocks of 256 for a token's heads.
-int64_t join_threads(int64_t T, int64_t q_heads, int64_t D)
-{
-    return T * ((q_heads * (D / 4) + 255) / 256) * 256;
-}
-
 // Sizes of an attention step that say how much workspace it takes.
 int check_attention_sizes(int64_t T, int32_t q_heads, int32_t heads, int32_t D, int64_t max_new, int64_t max_len,
                           int64_t chunk)
@@ -179,7 +173,7 @@ size_t lora_kv_attention_workspace_bytes(int64_t T, int32_t q_heads, int32_t hea
         chunk = kv_attention_chunk(max_new, q_heads, heads, head_dim, max_len);
     if (max_len <= chunk)
         return 0;
-    if (join_threads(T, q_heads, head_dim) > kMaxThreads || T * q_heads * ((max_len + chunk - 1) / chunk) > kMaxThreads)
+    if (T * q_heads > kMaxThreads / kWaveGroup || T * q_heads * ((max_len + chunk - 1) / chunk) > kMaxThreads)
         return 0;                            // more than a launch takes
     return (size_t)kv_attention_workspace(T, q_heads, head_dim, max_len, chunk);
 }
@@ -215,7 +209,7 @@ int lora_kv_attention(const lora_kv_cache* cache, const uint16_t* q, int64_t ld_
     const int64_t capacity = cache->max_pages * cache->page_size;
     max_len = max_len < capacity ? max_len : capacity;
     if (kv_attention_blocks(T, cache->n_seqs, max_new, q_heads, H, D, max_len, chunk) > kMaxThreads / kWaveGroup ||
-        (max_len > chunk && join_threads(T, q_heads, D) > kMaxThreads))
+        (max_len > chunk && T * q_heads > kMaxThreads / kWaveGroup))
         return LORA_ERR_SHAPE;
     const int64_t need = kv_attention_workspace(T, q_heads, D, max_len, chunk);
     if (need && !workspace)

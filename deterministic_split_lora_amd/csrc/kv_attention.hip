@@ -70,14 +70,13 @@ struct Work {
 // Rows of the sequences lie in tiles of R; tiles of a sequence begin at a slot that
 // grows with it.
 template <int R>
-__device__ __forceinline__ Work find_work(const KvAttentionParams& p, int64_t slot, int G)
+__device__ __forceinline__ Work find_work(const KvAttentionParams& p, int64_t slot, int64_t slots, int G)
 {
     auto at = [&](int64_t j, int64_t cu) { return cu * G / R + j; };
     Work w{};
-    w.b = kv_find(p.cache, slot, at);
-    if (w.b >= p.cache.n_seqs)
-        return w;
-    w.s = kv_sequence(p.cache, w.b, p.T);
+    const KvFound found = kv_find(p.cache, p.T, slot, slots, at);
+    w.b = found.b;
+    w.s = found.s;
     w.row0 = (slot - at(w.b, w.s.first)) * R;
     const int64_t left = w.s.n * G - w.row0;
     w.rows = w.row0 >= 0 && left > 0 ? (int)min(left, (int64_t)R) : 0;
@@ -100,216 +99,255 @@ __device__ __forceinline__ Seen seen_by(const KvAttentionParams& p, const KvSequ
 
 __host__ __device__ constexpr int64_t partial_floats(int D) { return D + 4; }
 
-// Split: the waves share the tile's rows and deal out the steps of the chunk;
-// otherwise every wave has rows of its own and takes all steps.
-template <int D, int NT, bool SPLIT>
-__global__ void __launch_bounds__(kWaves * 64) k_attention(KvAttentionParams p, uint32_t slots)
+typedef __bf16 bf16x4 __attribute__((ext_vector_type(4)));
+
+// Four values of a finished row from column c on, and with the first its lse.
+__device__ __forceinline__ void write_row(const KvAttentionParams& p, int64_t at, int h, int c, const f32x4& x, float top,
+                                          float total, int D)
 {
-    constexpr int R = 16 * NT * (SPLIT ? 1 : kWaves);
+    const float inv = total == 0.0f ? 0.0f : 1.0f / total;
+    *reinterpret_cast<bf16x4*>(p.out + at * p.ld_out + (int64_t)h * D + c) =
+        bf16x4{(__bf16)(x[0] * inv), (__bf16)(x[1] * inv), (__bf16)(x[2] * inv), (__bf16)(x[3] * inv)};
+    if (p.lse && c == 0)
+        p.lse[at * p.ld_lse + h] = total == 0.0f ? -INFINITY : (top + log2f(total)) * kLn2;
+}
+
+// Few rows (single tokens, drafts): bound by the cache's bytes.  The waves share the
+// tile's rows and deal out the steps of the chunk.  K of a wave's next step is asked
+// for as soon as this step's S are there, V as soon as it is multiplied, so one of
+// them is always on its way without registers of its own.
+// A sequence has `tiles` workgroups a head and chunk, enough for max_new tokens; where it has
+// more they go round again.
+template <int D, int NT>
+__global__ void __launch_bounds__(kWaves * 64, D * NT <= 128 ? 2 : 1) k_attention(KvAttentionParams p, uint32_t tiles)
+{
+    constexpr int R = 16 * NT;
     constexpr int kLoads = D / 64;           // 16-byte loads of a key by its 4 lanes
     constexpr int kOut = D / 16;             // tiles of 16 d
+    __shared__ float ml[kWaves][R][2];
+    __shared__ float ow[kWaves][16][D + 4];
     const int H = p.cache.heads, G = p.q_heads / H;
-    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, li = lane & 15, g = lane >> 4;
+    const int lane = threadIdx.x & 63, li = lane & 15, g = lane >> 4;
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int head = (int)(blockIdx.x % (uint32_t)H);
-    const uint32_t tile = blockIdx.x / (uint32_t)H;
-    const int64_t slot = tile % slots, chunk = tile / slots;
-
-    const Work w = find_work<R>(p, slot, G);
-    if (w.rows == 0)
-        return;
-    // rows of all sequences fit 31 bits
-    const int first_token = (int)w.row0 / G, last_token = ((int)w.row0 + w.rows - 1) / G;
-    const Seen first = seen_by(p, w.s, first_token), last = seen_by(p, w.s, last_token);
-    const int64_t begin = max(chunk * p.chunk, (int64_t)first.lo / kStep * kStep);
-    const int64_t end = min((chunk + 1) * p.chunk, (int64_t)last.hi + 1);
+    const uint32_t slot = blockIdx.x / (uint32_t)H, of_chunk = tiles * (uint32_t)p.cache.n_seqs;
+    const int64_t chunk = slot / of_chunk;
+    Work w{};
+    w.b = slot % of_chunk / tiles;
+    w.s = kv_sequence(p.cache, w.b, p.T);
     const bool several = p.partial != nullptr;
-    if (several && begin >= end)
-        return;
+    // rows of all sequences fit 31 bits
+    const int all_rows = (int)w.s.n * G;
+#pragma unroll 1
+    for (int row0 = (int)(slot % tiles) * R; row0 < all_rows; row0 += (int)tiles * R) {
+        w.row0 = row0;
+        w.rows = min(all_rows - row0, R);
+        const int first_token = row0 / G, last_token = (row0 + w.rows - 1) / G;
+        const Seen first = seen_by(p, w.s, first_token), last = seen_by(p, w.s, last_token);
+        const int64_t begin = max(chunk * p.chunk, (int64_t)first.lo / kStep * kStep);
+        const int64_t end = min((chunk + 1) * p.chunk, (int64_t)last.hi + 1);
+        if (several && begin >= end)
+            continue;
 
-    // the rows of this lane's columns
-    int64_t row_at[NT];                      // token's row of q and out
-    int row_head[NT];
-    Seen seen[NT];
-    bf16x8 q[NT][2 * kLoads];
-#pragma unroll
-    for (int n = 0; n < NT; ++n) {
-        const int r = (SPLIT ? 0 : wave * NT * 16) + n * 16 + li;
-        const bool in = r < w.rows;
-        const int row = (int)w.row0 + (in ? r : 0), token = row / G;
-        row_at[n] = in ? w.s.first + token : -1;
-        row_head[n] = head * G + row - token * G;
-        seen[n] = seen_by(p, w.s, token);
-        if (!in)
-            seen[n].hi = -1;
-        const uint16_t* src = p.q + (w.s.first + token) * p.ld_q + (int64_t)row_head[n] * D + 16 * g;
-#pragma unroll
-        for (int j = 0; j < kLoads; ++j) {
-            q[n][2 * j] = load_bf16x8(src + 64 * j);
-            q[n][2 * j + 1] = load_bf16x8(src + 64 * j + 8);
-        }
-    }
-
-    f32x4 o[NT][kOut];
-    float m[NT], l[NT];                      // l: of this lane's keys
-#pragma unroll
-    for (int n = 0; n < NT; ++n) {
-        m[n] = -INFINITY;
-        l[n] = 0.0f;
-#pragma unroll
-        for (int d = 0; d < kOut; ++d)
-            o[n][d] = f32x4{0, 0, 0, 0};
-    }
-    const float sl = p.scale * kLog2e;
-    const int P = p.cache.page_size;
-
-    int64_t s0 = begin / kStep;
-    if (SPLIT)
-        s0 += (wave - (int)(s0 % kWaves) + kWaves) % kWaves;
-    for (int64_t step = s0; step * kStep < end; step += SPLIT ? kWaves : 1) {
-        const int64_t p0 = step * kStep;
-        // keys: this lane's row of the products is of block li / 4; values: of block g
-        const int64_t pk = p0 + li / 4 * kKvBlock, pv = p0 + g * kKvBlock;
-        const int32_t page_k = kv_page(p.cache, w.b, pk), page_v = kv_page(p.cache, w.b, pv);
-        const int64_t ik = max(page_k, 0), iv = max(page_v, 0);
-        const int wk = (int)(pk & (P - 1)), wv = (int)(pv & (P - 1));
-        const uint8_t* kp = p.cache.k + ik * p.cache.ld_k + ((int64_t)head * P + wk + li % 4) * D + 16 * g;
-        const uint8_t* vp = p.cache.v + iv * p.cache.ld_v + ((int64_t)head * P + wv) * D + 16 * li;
-        const float ks = pow2_of_scale(p.cache.k_scales[ik * p.cache.ld_ks + (head * P + wk) / kKvBlock]);
-        float vs = pow2_of_scale(p.cache.v_scales[iv * p.cache.ld_vs + (head * P + wv) / kKvBlock]);
+        const int P = p.cache.page_size;
+        // this lane's row of the S products is a key of block li / 4, its V is of block g
+        int page_k = -1, page_v = -1;            // of the step that is loaded next
         u32x4 kc[4][kLoads], vc[kOut];
+        float ks = 1.0f, vs = 1.0f;
+        auto pages_of = [&](int step) {
+            page_k = kv_page(p.cache, w.b, (int64_t)step * kStep + li / 4 * kKvBlock);
+            page_v = kv_page(p.cache, w.b, (int64_t)step * kStep + g * kKvBlock);
+        };
+        auto load_k = [&](int step) {
+            const int64_t i = max(page_k, 0);
+            const int at = head * P + ((step * kStep + li / 4 * kKvBlock) & (P - 1));    // in tokens of all heads
+            const uint8_t* src = p.cache.k + i * p.cache.ld_k + (int64_t)(at + li % 4) * D + 16 * g;
+            ks = pow2_of_scale(p.cache.k_scales[i * p.cache.ld_ks + at / kKvBlock]);
 #pragma unroll
-        for (int t = 0; t < 4; ++t)
+            for (int t = 0; t < 4; ++t)
 #pragma unroll
-            for (int j = 0; j < kLoads; ++j)
-                kc[t][j] = *(const global_u32x4*)(kp + 4 * t * D + 64 * j);
-#pragma unroll
-        for (int d = 0; d < kOut; ++d)
-            vc[d] = *(const global_u32x4*)(vp + 16 * 16 * d);
-
-        f32x4 s[NT][4];
-#pragma unroll
-        for (int t = 0; t < 4; ++t) {
-#pragma unroll
-            for (int n = 0; n < NT; ++n)
-                s[n][t] = f32x4{0, 0, 0, 0};
-#pragma unroll
-            for (int j = 0; j < kLoads; ++j) {
-                const bf16x8 k0 = widen(kc[t][j][0], kc[t][j][1], ks), k1 = widen(kc[t][j][2], kc[t][j][3], ks);
-#pragma unroll
-                for (int n = 0; n < NT; ++n) {
-                    s[n][t] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(k0, q[n][2 * j], s[n][t], 0, 0, 0);
-                    s[n][t] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(k1, q[n][2 * j + 1], s[n][t], 0, 0, 0);
-                }
-            }
-        }
-
-        // every row of the tile sees every key of most steps
-        const bool edge = p0 < last.lo || p0 + kStep - 1 > first.hi || __any(page_v < 0);
-        uint32_t bad = 0;
-        if (edge) {
-#pragma unroll
-            for (int n = 0; n < NT; ++n)
-#pragma unroll
-                for (int t = 0; t < 4; ++t)
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        const int key = (int)pv + 4 * t + i;
-                        const bool in = page_v >= 0 && key >= seen[n].lo && key <= seen[n].hi;
-                        s[n][t][i] = in ? s[n][t][i] : -INFINITY;
-                    }
-            // a block that was never written may hold anything, its scale too
-            const bool unseen = page_v < 0 || pv > last.hi;
-            vs = unseen ? 1.0f : vs;
+                for (int j = 0; j < kLoads; ++j)
+                    kc[t][j] = *(const global_u32x4*)(src + 4 * t * D + 64 * j);
+        };
+        auto load_v = [&](int step) {
+            const int64_t i = max(page_v, 0);
+            const int at = head * P + ((step * kStep + g * kKvBlock) & (P - 1));
+            const uint8_t* src = p.cache.v + i * p.cache.ld_v + (int64_t)at * D + 16 * li;
+            vs = pow2_of_scale(p.cache.v_scales[i * p.cache.ld_vs + at / kKvBlock]);
 #pragma unroll
             for (int d = 0; d < kOut; ++d)
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    vc[d][i] = unseen ? 0u : vc[d][i];
-                    bad |= nan_bytes(vc[d][i]);
-                }
+                vc[d] = *(const global_u32x4*)(src + 16 * 16 * d);
+        };
+        // steps are dealt by their number, wherever the first one lies
+        const int s1 = (int)((end + kStep - 1) / kStep);
+        int step = (int)(begin / kStep);
+        step += (wave - step % kWaves + kWaves) % kWaves;
+        if (step < s1) {
+            pages_of(step);
+            load_k(step);
+            load_v(step);
         }
-        bf16x8 prob[NT][2];
+
+        // the rows of this lane's columns
+        Seen seen[NT];
+        bf16x8 q[NT][2 * kLoads];
 #pragma unroll
         for (int n = 0; n < NT; ++n) {
-            float top = -INFINITY;
+            const int r = n * 16 + li;
+            const bool in = r < w.rows;
+            const int row = (int)w.row0 + (in ? r : 0), token = row / G, q_head = head * G + row - token * G;
+            seen[n] = seen_by(p, w.s, token);
+            if (!in)
+                seen[n].hi = -1;
+            const uint16_t* src = p.q + (w.s.first + token) * p.ld_q + (int64_t)q_head * D + 16 * g;
 #pragma unroll
-            for (int t = 0; t < 4; ++t)
+            for (int j = 0; j < kLoads; ++j) {
+                q[n][2 * j] = load_bf16x8(src + 64 * j);
+                q[n][2 * j + 1] = load_bf16x8(src + 64 * j + 8);
+            }
+        }
+
+        f32x4 o[NT][kOut];
+        float m[NT], l[NT];                      // l: of this lane's keys
 #pragma unroll
-                for (int i = 0; i < 4; ++i)
-                    top = fmaxf(top, s[n][t][i]);
-            const float mn = fmaxf(m[n], group_max(top) * sl);
-            const float shift = shift_of(mn), f = exp2f(m[n] - shift);
-            m[n] = mn;
-            float sum = 0.0f;
-#pragma unroll
-            for (int t = 0; t < 4; ++t)
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const float e = __builtin_amdgcn_exp2f(fmaf(s[n][t][i], sl, -shift));
-                    sum += e;
-                    prob[n][t / 2][4 * (t % 2) + i] = (__bf16)e;
-                }
-            l[n] = l[n] * f + sum;
+        for (int n = 0; n < NT; ++n) {
+            m[n] = -INFINITY;
+            l[n] = 0.0f;
 #pragma unroll
             for (int d = 0; d < kOut; ++d)
-#pragma unroll
-                for (int i = 0; i < 4; ++i)
-                    o[n][d][i] *= f;
+                o[n][d] = f32x4{0, 0, 0, 0};
         }
-        if (edge && __any(bad != 0)) {
-            // a value that is NaN reaches the rows that see its key, and no others
+        const float sl = p.scale * kLog2e;
+
+#pragma unroll 1
+        for (; step < s1; step += kWaves) {
+            const int p0 = step * kStep, pv = p0 + g * kKvBlock;
+            const bool missing = page_v < 0, more = step + kWaves < s1;
+            if (more)
+                pages_of(step + kWaves);
+            f32x4 s[NT][4];
+#pragma unroll
+            for (int t = 0; t < 4; ++t) {
+#pragma unroll
+                for (int n = 0; n < NT; ++n)
+                    s[n][t] = f32x4{0, 0, 0, 0};
+#pragma unroll
+                for (int j = 0; j < kLoads; ++j) {
+                    const bf16x8 k0 = widen(kc[t][j][0], kc[t][j][1], ks), k1 = widen(kc[t][j][2], kc[t][j][3], ks);
+#pragma unroll
+                    for (int n = 0; n < NT; ++n) {
+                        s[n][t] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(k0, q[n][2 * j], s[n][t], 0, 0, 0);
+                        s[n][t] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(k1, q[n][2 * j + 1], s[n][t], 0, 0, 0);
+                    }
+                }
+            }
+            if (more)
+                load_k(step + kWaves);
+
+            // every row of the tile sees every key of most steps
+            const bool edge = p0 < last.lo || p0 + kStep - 1 > first.hi || __any(missing);
+            uint32_t bad = 0;
+            if (edge) {
+#pragma unroll
+                for (int n = 0; n < NT; ++n)
+#pragma unroll
+                    for (int t = 0; t < 4; ++t)
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) {
+                            const int key = pv + 4 * t + i;
+                            const bool in = !missing && key >= seen[n].lo && key <= seen[n].hi;
+                            s[n][t][i] = in ? s[n][t][i] : -INFINITY;
+                        }
+                // a block that was never written may hold anything, its scale too
+                const bool unseen = missing || pv > last.hi;
+                vs = unseen ? 1.0f : vs;
+#pragma unroll
+                for (int d = 0; d < kOut; ++d)
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        vc[d][i] = unseen ? 0u : vc[d][i];
+                        bad |= nan_bytes(vc[d][i]);
+                    }
+            }
+            bf16x8 prob[NT][2];
 #pragma unroll
             for (int n = 0; n < NT; ++n) {
-                bf16x8 sees[2];
+                float top = -INFINITY;
+#pragma unroll
+                for (int t = 0; t < 4; ++t)
+#pragma unroll
+                    for (int i = 0; i < 4; ++i)
+                        top = fmaxf(top, s[n][t][i]);
+                const float mn = fmaxf(m[n], group_max(top) * sl);
+                const float shift = shift_of(mn), f = __builtin_amdgcn_exp2f(m[n] - shift);
+                m[n] = mn;
+                float sum = 0.0f;
 #pragma unroll
                 for (int t = 0; t < 4; ++t)
 #pragma unroll
                     for (int i = 0; i < 4; ++i) {
-                        const int key = (int)pv + 4 * t + i;
-                        const bool in = page_v >= 0 && key >= seen[n].lo && key <= seen[n].hi;
-                        sees[t / 2][4 * (t % 2) + i] = in ? (__bf16)1.0f : (__bf16)0.0f;
+                        const float e = __builtin_amdgcn_exp2f(fmaf(s[n][t][i], sl, -shift));
+                        sum += e;
+                        prob[n][t / 2][4 * (t % 2) + i] = (__bf16)e;
                     }
+                l[n] = l[n] * f + sum;
 #pragma unroll
-                for (int d = 0; d < kOut; ++d) {
-                    f32x4 hit = {0, 0, 0, 0};
-#pragma unroll
-                    for (int u = 0; u < 2; ++u) {
-                        const bf16x8 one =
-                            widen(nan_bytes(vc[d][2 * u]) >> 7 << 5 & 0x20202020u,
-                                  nan_bytes(vc[d][2 * u + 1]) >> 7 << 5 & 0x20202020u, 1.0f);
-                        hit = __builtin_amdgcn_mfma_f32_16x16x32_bf16(one, sees[u], hit, 0, 0, 0);
-                    }
+                for (int d = 0; d < kOut; ++d)
 #pragma unroll
                     for (int i = 0; i < 4; ++i)
-                        o[n][d][i] = hit[i] > 0.0f ? __builtin_nanf("") : o[n][d][i];
+                        o[n][d][i] *= f;
+            }
+            if (edge && __any(bad != 0)) {
+                // a value that is NaN reaches the rows that see its key, and no others
+#pragma unroll
+                for (int n = 0; n < NT; ++n) {
+                    bf16x8 sees[2];
+#pragma unroll
+                    for (int t = 0; t < 4; ++t)
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) {
+                            const int key = pv + 4 * t + i;
+                            const bool in = !missing && key >= seen[n].lo && key <= seen[n].hi;
+                            sees[t / 2][4 * (t % 2) + i] = in ? (__bf16)1.0f : (__bf16)0.0f;
+                        }
+#pragma unroll
+                    for (int d = 0; d < kOut; ++d) {
+                        f32x4 hit = {0, 0, 0, 0};
+#pragma unroll
+                        for (int u = 0; u < 2; ++u) {
+                            // a code of 2^-3 where there is a NaN
+                            const bf16x8 one =
+                                widen(nan_bytes(vc[d][2 * u]) >> 2, nan_bytes(vc[d][2 * u + 1]) >> 2, 1.0f);
+                            hit = __builtin_amdgcn_mfma_f32_16x16x32_bf16(one, sees[u], hit, 0, 0, 0);
+                        }
+#pragma unroll
+                        for (int i = 0; i < 4; ++i)
+                            o[n][d][i] = hit[i] > 0.0f ? __builtin_nanf("") : o[n][d][i];
+                    }
                 }
+#pragma unroll
+                for (int d = 0; d < kOut; ++d)
+#pragma unroll
+                    for (int i = 0; i < 4; ++i)
+                        vc[d][i] &= ~((nan_bytes(vc[d][i]) >> 7) * 0xFFu);
             }
 #pragma unroll
-            for (int d = 0; d < kOut; ++d)
+            for (int d = 0; d < kOut; ++d) {
+                const bf16x8 v0 = widen(vc[d][0], vc[d][1], vs), v1 = widen(vc[d][2], vc[d][3], vs);
 #pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const uint32_t b = nan_bytes(vc[d][i]);
-                    vc[d][i] &= ~((b >> 7) * 0xFFu);
+                for (int n = 0; n < NT; ++n) {
+                    o[n][d] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(v0, prob[n][0], o[n][d], 0, 0, 0);
+                    o[n][d] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(v1, prob[n][1], o[n][d], 0, 0, 0);
                 }
-        }
-#pragma unroll
-        for (int d = 0; d < kOut; ++d) {
-            const bf16x8 v0 = widen(vc[d][0], vc[d][1], vs), v1 = widen(vc[d][2], vc[d][3], vs);
-#pragma unroll
-            for (int n = 0; n < NT; ++n) {
-                o[n][d] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(v0, prob[n][0], o[n][d], 0, 0, 0);
-                o[n][d] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(v1, prob[n][1], o[n][d], 0, 0, 0);
             }
+            if (more)
+                load_v(step + kWaves);
         }
-    }
 #pragma unroll
-    for (int n = 0; n < NT; ++n)
-        l[n] = group_sum(l[n]);
+        for (int n = 0; n < NT; ++n)
+            l[n] = group_sum(l[n]);
 
-    if constexpr (SPLIT) {
         // the waves' shares are joined in ascending order
-        __shared__ float ml[kWaves][R][2];
-        __shared__ float ow[kWaves][16][D + 4];
 #pragma unroll
         for (int n = 0; n < NT; ++n)
             if (g == 0) {
@@ -358,44 +396,12 @@ __global__ void __launch_bounds__(kWaves * 64) k_attention(KvAttentionParams p, 
                             dst[1] = total;
                         }
                     } else {
-                        const float inv = total == 0.0f ? 0.0f : 1.0f / total;
-                        typedef __bf16 bf16x4 __attribute__((ext_vector_type(4)));
-                        *reinterpret_cast<bf16x4*>(p.out + at * p.ld_out + (int64_t)h * D + c + c0) =
-                            bf16x4{(__bf16)(x[0] * inv), (__bf16)(x[1] * inv), (__bf16)(x[2] * inv), (__bf16)(x[3] * inv)};
-                        if (p.lse && c + c0 == 0)
-                            p.lse[at * p.ld_lse + h] = total == 0.0f ? -INFINITY : (top + log2f(total)) * kLn2;
+                        write_row(p, at, h, c + c0, x, top, total, D);
                     }
                 }
             }
         }
-    } else {
-#pragma unroll
-        for (int n = 0; n < NT; ++n) {
-            if (row_at[n] < 0)
-                continue;
-            if (several) {
-                float* dst = p.partial + ((chunk * p.T + row_at[n]) * p.q_heads + row_head[n]) * partial_floats(D);
-#pragma unroll
-                for (int d = 0; d < kOut; ++d)
-                    *reinterpret_cast<f32x4*>(dst + 4 + 16 * d + 4 * g) = o[n][d];
-                if (g == 0) {
-                    dst[0] = m[n];
-                    dst[1] = l[n];
-                }
-            } else {
-                const float inv = l[n] == 0.0f ? 0.0f : 1.0f / l[n];
-                uint16_t* dst = p.out + row_at[n] * p.ld_out + (int64_t)row_head[n] * D;
-                typedef __bf16 bf16x4 __attribute__((ext_vector_type(4)));
-#pragma unroll
-                for (int d = 0; d < kOut; ++d)
-                    *reinterpret_cast<bf16x4*>(dst + 16 * d + 4 * g) =
-                        bf16x4{(__bf16)(o[n][d][0] * inv), (__bf16)(o[n][d][1] * inv), (__bf16)(o[n][d][2] * inv),
-                               (__bf16)(o[n][d][3] * inv)};
-                if (p.lse && g == 0)
-                    p.lse[row_at[n] * p.ld_lse + row_head[n]] =
-                        l[n] == 0.0f ? -INFINITY : (m[n] + log2f(l[n])) * kLn2;
-            }
-        }
+        __syncthreads();                         // before the next tile's shares
     }
 }
 
@@ -456,7 +462,7 @@ __global__ void __launch_bounds__(kWaves * 64, D == 256 ? 1 : 2) k_attention_til
     // a prompt's last rows see the most keys: they begin first
     const int64_t slot = slots - 1 - tile % slots, chunk = tile / slots;
 
-    const Work w = find_work<kTileRows>(p, slot, G);
+    const Work w = find_work<kTileRows>(p, slot, slots, G);
     if (w.rows == 0)
         return;
     const int first_token = (int)w.row0 / G, last_token = ((int)w.row0 + w.rows - 1) / G;
@@ -708,120 +714,136 @@ __global__ void __launch_bounds__(kWaves * 64, D == 256 ? 1 : 2) k_attention_til
     l = half_sum(l);
     if (!in)
         return;
-    typedef __bf16 bf16x4 __attribute__((ext_vector_type(4)));
     const int64_t out_row = w.s.first + token;
-    if (several) {
-        float* dst = p.partial + ((chunk * p.T + out_row) * p.q_heads + q_head) * partial_floats(D);
-#pragma unroll
-        for (int d = 0; d < kOut; ++d)
-#pragma unroll
-            for (int i = 0; i < 4; ++i)
-                *reinterpret_cast<f32x4*>(dst + 4 + 32 * d + 8 * i + 4 * h) =
-                    f32x4{o[d][4 * i], o[d][4 * i + 1], o[d][4 * i + 2], o[d][4 * i + 3]};
-        if (h == 0) {
-            dst[0] = m;
-            dst[1] = l;
-        }
-    } else {
-        const float inv = l == 0.0f ? 0.0f : 1.0f / l;
-        uint16_t* dst = p.out + out_row * p.ld_out + (int64_t)q_head * D;
-#pragma unroll
-        for (int d = 0; d < kOut; ++d)
-#pragma unroll
-            for (int i = 0; i < 4; ++i)
-                *reinterpret_cast<bf16x4*>(dst + 32 * d + 8 * i + 4 * h) =
-                    bf16x4{(__bf16)(o[d][4 * i] * inv), (__bf16)(o[d][4 * i + 1] * inv), (__bf16)(o[d][4 * i + 2] * inv),
-                           (__bf16)(o[d][4 * i + 3] * inv)};
-        if (p.lse && h == 0)
-            p.lse[out_row * p.ld_lse + q_head] = l == 0.0f ? -INFINITY : (m + log2f(l)) * kLn2;
+    float* dst = p.partial + ((chunk * p.T + out_row) * p.q_heads + q_head) * partial_floats(D);
+    if (several && h == 0) {
+        dst[0] = m;
+        dst[1] = l;
     }
+#pragma unroll
+    for (int d = 0; d < kOut; ++d)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const f32x4 x = {o[d][4 * i], o[d][4 * i + 1], o[d][4 * i + 2], o[d][4 * i + 3]};
+            const int c = 32 * d + 8 * i + 4 * h;
+            if (several)
+                *reinterpret_cast<f32x4*>(dst + 4 + c) = x;
+            else
+                write_row(p, out_row, q_head, c, x, m, l, D);
+        }
 }
 
-// Joins the chunks of each row in ascending order: D / 4 threads a row, a block for
-// heads of one token.
+// Joins the chunks of a row: kGroups groups of D / 4 threads take its chunks in turn, by
+// their number, and are joined in ascending order, so that the chunks of a token far into
+// a long cache are read together.  A block has heads of one token.
 template <int D>
 __global__ void __launch_bounds__(256) k_join(KvAttentionParams p)
 {
-    constexpr int kThreads = D / 4, kHeads = 256 / kThreads;
-    const uint32_t groups = ((uint32_t)p.q_heads + kHeads - 1) / kHeads;
-    const int64_t at = blockIdx.x / groups;
-    const int h = (int)(blockIdx.x % groups) * kHeads + threadIdx.x / kThreads;
-    const int c = threadIdx.x % kThreads * 4;
-    const int64_t row = at * p.q_heads + h;
-    const int64_t b = kv_find(p.cache, at, [](int64_t, int64_t cu) { return cu; });
-    if (h >= p.q_heads || b >= p.cache.n_seqs)
-        return;
-    const KvSequence s = kv_sequence(p.cache, b, p.T);
+    constexpr int kGroups = 4, kThreads = D / 4, kHeads = 256 / (kThreads * kGroups);
+    __shared__ __align__(16) float part[kHeads][kGroups][D];
+    __shared__ float ml[kHeads][kGroups][2];
+    const uint32_t blocks = ((uint32_t)p.q_heads + kHeads - 1) / kHeads;
+    const int64_t at = blockIdx.x / blocks;
+    const int group = threadIdx.x / kThreads % kGroups, c = threadIdx.x % kThreads * 4;
+    const int my = threadIdx.x / (kThreads * kGroups), h = (int)(blockIdx.x % blocks) * kHeads + my;
+    const KvSequence s = kv_find(p.cache, p.T, at, p.T, [](int64_t, int64_t cu) { return cu; }).s;
     if (s.n == 0 || at < s.first)
         return;
     const Seen seen = seen_by(p, s, at - s.first);
-    const int64_t c0 = seen.lo / p.chunk, c1 = seen.hi < seen.lo ? c0 : seen.hi / p.chunk + 1;
+    const int c0 = (int)(seen.lo / p.chunk), c1 = seen.hi < seen.lo ? c0 : (int)(seen.hi / p.chunk) + 1;
     const int64_t pitch = p.T * p.q_heads * partial_floats(D);
-    const float* src = p.partial + row * partial_floats(D);
-    float top = -INFINITY;
-    for (int64_t i = c0; i < c1; ++i)
-        top = fmaxf(top, src[i * pitch]);
-    const float shift = shift_of(top);
-    float total = 0.0f;
+    const float* src = p.partial + (at * p.q_heads + h) * partial_floats(D);
+    float top = -INFINITY, total = 0.0f;
     f32x4 x = {0, 0, 0, 0};
+    const int last = h < p.q_heads ? c1 : 0;
 #pragma unroll 4
-    for (int64_t i = c0; i < c1; ++i) {
-        const float f = exp2f(src[i * pitch] - shift);
+    for (int i = c0 + (group - c0 % kGroups + kGroups) % kGroups; i < last; i += kGroups) {
+        const float mi = src[i * pitch], li = src[i * pitch + 1];
         const f32x4 y = *reinterpret_cast<const f32x4*>(src + i * pitch + 4 + c);
-        total += src[i * pitch + 1] * f;
+        const float now = fmaxf(top, mi), shift = shift_of(now);
+        const float f = __builtin_amdgcn_exp2f(top - shift), fi = __builtin_amdgcn_exp2f(mi - shift);
+        top = now;
+        total = total * f + li * fi;
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+            x[e] = x[e] * f + y[e] * fi;
+    }
+    *reinterpret_cast<f32x4*>(&part[my][group][c]) = x;
+    if (c == 0) {
+        ml[my][group][0] = top;
+        ml[my][group][1] = total;
+    }
+    __syncthreads();
+    if (group > 0 || h >= p.q_heads)
+        return;
+    for (int i = 0; i < kGroups; ++i)
+        top = fmaxf(top, ml[my][i][0]);
+    const float shift = shift_of(top);
+    total = 0.0f;
+    x = f32x4{0, 0, 0, 0};
+#pragma unroll
+    for (int i = 0; i < kGroups; ++i) {
+        const float f = __builtin_amdgcn_exp2f(ml[my][i][0] - shift);
+        const f32x4 y = *reinterpret_cast<const f32x4*>(&part[my][i][c]);
+        total += ml[my][i][1] * f;
 #pragma unroll
         for (int e = 0; e < 4; ++e)
             x[e] += y[e] * f;
     }
-    const float inv = total == 0.0f ? 0.0f : 1.0f / total;
-    typedef __bf16 bf16x4 __attribute__((ext_vector_type(4)));
-    *reinterpret_cast<bf16x4*>(p.out + at * p.ld_out + (int64_t)h * D + c) =
-        bf16x4{(__bf16)(x[0] * inv), (__bf16)(x[1] * inv), (__bf16)(x[2] * inv), (__bf16)(x[3] * inv)};
-    if (p.lse && c == 0)
-        p.lse[at * p.ld_lse + h] = total == 0.0f ? -INFINITY : (top + log2f(total)) * kLn2;
+    write_row(p, at, h, c, x, top, total, D);
 }
 
 // Rows of a tile that these sizes get; up to 64 rows a sequence the waves split the keys.
+// (Two tiles of 16 rows of 256 would not fit the registers.)
 int tile_rows(int64_t max_new, int G, int D)
 {
     const int64_t rows = max_new * G;
-    return rows <= 16 ? 16 : rows <= 64 ? 32 : kTileRows;
+    return rows <= 16 || (rows <= 64 && D == 256) ? 16 : rows <= 64 ? 32 : kTileRows;
 }
 
-int64_t tile_slots(int64_t T, int64_t n_seqs, int R, int G)
+bool few_rows(int R) { return R <= 32; }
+
+// Workgroups of a head and chunk: few rows have so many for each sequence, tiles of many
+// rows lie behind one another over all of them.
+int64_t tile_slots(int64_t T, int64_t n_seqs, int64_t max_new, int R, int G)
 {
-    return T * G / R + n_seqs;
+    return few_rows(R) ? n_seqs * ((max_new * G + R - 1) / R) : T * G / R + n_seqs;
 }
 
 template <int D>
 hipError_t launch(const KvAttentionParams& p, hipStream_t st)
 {
     const int G = p.q_heads / p.cache.heads, R = tile_rows(p.max_new, G, D);
-    const int64_t slots = tile_slots(p.T, p.cache.n_seqs, R, G);
+    const int64_t slots = tile_slots(p.T, p.cache.n_seqs, p.max_new, R, G);
+    const uint32_t tiles = (uint32_t)((p.max_new * G + R - 1) / R);
     const int64_t chunks = (p.max_len + p.chunk - 1) / p.chunk;
     const dim3 grid((unsigned)(slots * p.cache.heads * chunks)), threads(kWaves * 64);
     if (R == 16)
-        hipLaunchKernelGGL((k_attention<D, 1, true>), grid, threads, 0, st, p, (uint32_t)slots);
+        hipLaunchKernelGGL((k_attention<D, 1>), grid, threads, 0, st, p, tiles);
     else if (R == 32)
-        hipLaunchKernelGGL((k_attention<D, 2, true>), grid, threads, 0, st, p, (uint32_t)slots);
+        hipLaunchKernelGGL((k_attention<D == 256 ? 64 : D, 2>), grid, threads, 0, st, p, tiles);
     else
         hipLaunchKernelGGL(k_attention_tile<D>, grid, threads, 0, st, p, (uint32_t)slots);
-    if (p.partial) {
-        const int per = 256 / (D / 4);
-        hipLaunchKernelGGL(k_join<D>, dim3((unsigned)(p.T * ((p.q_heads + per - 1) / per))), dim3(256), 0, st, p);
-    }
+    if (p.partial)
+        hipLaunchKernelGGL(k_join<D>, dim3((unsigned)(p.T * ((p.q_heads * D + 255) / 256))), dim3(256), 0, st, p);
     return hipGetLastError();
 }
 
 }  // namespace
 
+// About one workgroup a CU for one sequence.  Shorter chunks cost a batch more than they
+// give a sequence alone: 512 keys instead of 256 take one of 1025 from 9.3 to 10.5 us
+// (so it keeps 256), but 61 of up to 16384 from 333 to 280 (2048: 250), 32 drafts of 5
+// tokens from 49 to 39 (2048: 33); one of 131071 takes 56 with 512, 48 with 2048 or 4096,
+// 74 with 8192.
 int64_t kv_attention_chunk(int64_t max_new, int32_t q_heads, int32_t kv_heads, int32_t D, int64_t max_len)
 {
     const int G = q_heads / kv_heads, R = tile_rows(max_new, G, D);
     const int64_t tiles = (max_new * G + R - 1) / R * kv_heads;
-    const int64_t splits = tiles < 512 ? 512 / tiles : 1;
-    const int64_t chunk = (max_len + splits - 1) / splits;
-    return (chunk + kKvChunkUnit - 1) / kKvChunkUnit * kKvChunkUnit;
+    // tiles of many rows run two to a CU
+    const int64_t wanted = few_rows(R) ? 256 : 512, splits = tiles < wanted ? wanted / tiles : 1;
+    const int64_t chunk = (max_len + splits - 1) / splits, least = max_len > 2048 ? 2 * kKvChunkUnit : kKvChunkUnit;
+    return ((chunk > least ? chunk : least) + kKvChunkUnit - 1) / kKvChunkUnit * kKvChunkUnit;
 }
 
 int64_t kv_attention_workspace(int64_t T, int32_t q_heads, int32_t D, int64_t max_len, int64_t chunk)
@@ -834,7 +856,7 @@ int64_t kv_attention_blocks(int64_t T, int64_t n_seqs, int64_t max_new, int32_t 
                             int64_t max_len, int64_t chunk)
 {
     const int G = q_heads / kv_heads;
-    return tile_slots(T, n_seqs, tile_rows(max_new, G, D), G) * kv_heads * ((max_len + chunk - 1) / chunk);
+    return tile_slots(T, n_seqs, max_new, tile_rows(max_new, G, D), G) * kv_heads * ((max_len + chunk - 1) / chunk);
 }
 
 hipError_t launch_kv_attention(const KvAttentionParams& p, hipStream_t st)

@@ -27,30 +27,61 @@ struct KvSequence {
     int64_t len;                             // tokens with them
 };
 
-__device__ __forceinline__ KvSequence kv_sequence(const KvCacheView& c, int64_t b, int64_t T)
+__device__ __forceinline__ KvSequence kv_sequence(int64_t first, int64_t end, int64_t len, int64_t T)
 {
-    KvSequence s;
-    s.first = c.cu_tokens[b];
-    const int64_t end = c.cu_tokens[b + 1];
-    s.len = c.seq_lens[b];
-    s.n = s.first >= 0 && end > s.first && end <= T ? end - s.first : 0;
-    return s;
+    return {first, first >= 0 && end > first && end <= T ? end - first : 0, len};
 }
 
-// Sequences have slots in a row: those of j begin at at(j, cu_tokens[j]), which does
-// not fall with j.  The one that slot w (the same in the whole wave, every lane of
-// which is active) belongs to; n_seqs where w lies behind them.
-// Every lane of the wave looks at entries of its own: one round of loads for 64.
-template <class F>
-__device__ __forceinline__ int64_t kv_find(const KvCacheView& c, int64_t w, F at)
+__device__ __forceinline__ KvSequence kv_sequence(const KvCacheView& c, int64_t b, int64_t T)
 {
-    int64_t b = 0;
-    const int lane = threadIdx.x & 63;
-    for (int64_t base = 1; base <= c.n_seqs; base += 64) {
-        const int64_t j = base + lane;
-        b += __popcll(__ballot(j <= c.n_seqs && at(j, (int64_t)c.cu_tokens[min(j, c.n_seqs)]) <= w));
+    return kv_sequence(c.cu_tokens[b], c.cu_tokens[b + 1], c.seq_lens[b], T);
+}
+
+// Sequences have slots in a row, `total` in all: those of j begin at at(j, cu_tokens[j]),
+// which does not fall with j.  The one that slot w (the same in the whole wave, every
+// lane of which is active) belongs to, and its entries; -1 where w lies behind them all.
+// A lane looks at a sequence and reads all that is needed of it, so where the sequences
+// have about as many slots each, one round of loads finds it; else the range is cut to a
+// 64th each round.
+struct KvFound {
+    int64_t b;
+    KvSequence s;
+};
+
+template <class F>
+__device__ __forceinline__ KvFound kv_find(const KvCacheView& c, int64_t T, int64_t w, int64_t total, F at)
+{
+    KvFound f{-1, {0, 0, 0}};
+    const int lane = threadIdx.x & 63, n = (int)c.n_seqs;
+    int base = min(max((int)((float)w / (float)total * (float)n) - 32, 0), n - 1);
+#pragma unroll 1
+    for (int from = 0, size = n;;) {
+        const int j = base + lane, i = min(j, n - 1);
+        const int32_t first = c.cu_tokens[i], end = c.cu_tokens[i + 1], len = c.seq_lens[i];
+        const uint64_t hit =
+            __ballot(j < n && at((int64_t)j, (int64_t)first) <= w && at((int64_t)j + 1, (int64_t)end) > w);
+        if (hit) {
+            const int l = __builtin_ctzll(hit);
+            f.b = base + l;
+            f.s = kv_sequence(__builtin_amdgcn_readlane(first, l), __builtin_amdgcn_readlane(end, l),
+                              __builtin_amdgcn_readlane(len, l), T);
+            return f;
+        }
+        if (size <= 64 && base <= from && base + 64 >= from + size)
+            return f;                        // looked at every one that is left
+        // the first of 64 parts of the range whose last sequence ends behind w
+        while (size > 64) {
+            const int part = (size + 63) / 64, k = min(from + (lane + 1) * part, from + size);
+            const uint64_t behind = __ballot(at((int64_t)k, (int64_t)c.cu_tokens[k]) > w);
+            if (behind == 0)
+                return f;
+            from += __builtin_ctzll(behind) * part;
+            size = min(part, n - from);
+            if (size <= 0)
+                return f;
+        }
+        base = from;
     }
-    return b;
 }
 
 // The page that holds a sequence's tokens [p, p + kKvBlock), or -1 if there is none;

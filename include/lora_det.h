@@ -776,8 +776,7 @@ int lora_kv_append(const lora_kv_cache* cache, const uint16_t* q, int64_t ld_q, 
  *             is less
  * q, out: bf16 [T][ld], q_heads * D columns, 16-byte aligned, ld a multiple of 8;
  * lse: fp32 [T][ld_lse] or NULL.  window needs causal.  scale: positive, finite.
- * q_heads a multiple of heads; T * q_heads < 2^31, with several chunks
- * T * (q_heads * head_dim rounded up to 1024) < 2^34.
+ * q_heads a multiple of heads; T * q_heads < 2^31, with several chunks below 2^24.
  * workspace: lora_kv_attention_workspace_bytes of the same sizes, 16-byte aligned, no
  * initialisation needed (NULL where that is 0; 0 is also returned for invalid input).
  * One launch, two with more than one chunk.
