@@ -205,7 +205,7 @@ PyObject* linear(PyObject*, PyObject* const* a, Py_ssize_t n)
 // xq, xs, wq, ws, y, split_k, workspace, stream
 PyObject* linear_q(PyObject*, PyObject* const* a, Py_ssize_t n)
 {
-    return call(n, 9, [&] {
+    return call(n, 8, [&] {
         const Matrix y = matrix(a[4], kBf16, "y");
         const int64_t K = 2 * matrix(a[0], at::kByte, "x").cols;
         const Mx4 x = mx4(a[0], a[1], K, "x"), w = mx4(a[2], a[3], K, "W");
