@@ -1,5 +1,6 @@
 """Deterministic Split-K LoRA shrink / expand for AMD MI355X (gfx950), and the
-operators around the adapters: MX4 products, the block norm, sampling.
+operators around the adapters: MX4 products, the block norm, sampling, a paged
+8-bit cache with attention over it, verification of drafted tokens.
 
 The computation lives in liblora_det.so (hand-written HIP kernels behind the C
 interface of include/lora_det.h); this package is its thin Python binding, with

@@ -18,6 +18,10 @@
 // in one half and values in the other, so nobody else writes there and no atomics
 // are needed; further workgroups take a token's queries.  A thread holds 16 values
 // that rotate among themselves.
+//
+// Measured on MI355X, with the queries: 8190 tokens of 64 + 2 x 8 heads of 128, normed,
+// 78-84 us (364 MB, 4.3-4.6 TB/s: the rate of a large copy); 251 single tokens of 32 + 2 x 8
+// heads 12; one token 5.2 (three rounds of loads that wait for one another, and the launch).
 #include "kv_cache.h"
 
 #include <math.h>

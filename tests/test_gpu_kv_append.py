@@ -107,6 +107,30 @@ def test_large_batch_and_long_prompt():
 
 
 @pytest.mark.parametrize("D", [64, 128, 256])
+@pytest.mark.parametrize("new", [[1] * 9, [0, 3, 0, 1, 2, 0, 0, 2, 1], [9] + [0] * 8, [0, 0, 40] + [0] * 37])
+def test_as_many_tokens_as_sequences(D, new):
+    """A step of single tokens, and others that only count as many: sequences without any, with blocks of several."""
+    lengths = [(n, n + 13 * b % 40) for b, n in enumerate(new)]
+    batch = Batch(lengths, 16, 2, D, seed=3).fill()
+    g = batch.gpu(pad=16)
+    assert batch.T == len(new)
+    run(batch, g, 3, True, rope_table(100, D), True, seed=5)
+    batch.same(g)
+
+
+def test_columns_of_a_wider_table():
+    """The page table as a view of a wider one."""
+    t = torch()
+    batch = Batch([(3, 40), (2, 33)], 16, 1, 64, seed=4).fill()
+    wide = t.full((2, 10), 7 << 20, dtype=t.int32, device="cuda")
+    wide[:, 2:2 + batch.table.shape[1]] = t.from_numpy(batch.table).cuda()
+    g = batch.gpu()
+    g = g._replace(page_table=wide[:, 2:2 + batch.table.shape[1]])
+    run(batch, g, 1, False, None, False, seed=5)
+    batch.same(g)
+
+
+@pytest.mark.parametrize("D", [64, 128, 256])
 def test_codes_are_the_nearest(D):
     """Values of one block against the formula in 64 bits: half a step of the code, the scale the least that fits."""
     batch = Batch([(16, 16), (5, 5), (16, 16)], 16, 1, D, seed=9)
