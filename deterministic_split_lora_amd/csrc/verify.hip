@@ -8,9 +8,10 @@
 //
 // Three launches.  The rows' maxima, cuts and weights: a workgroup a row, the same
 // steps as a draw (sample_row.h), all rows at once, since which ones count is only
-// known from them.  Then the sums of max(P - Q, 0) over segments of the one row a
-// sequence draws from, and the draw itself from its segment; each of these works
-// out the accepted tokens anew, a lane a token, which is cheaper than a launch.
+// known from them; with its cuts a row leaves what it gives its drafted token.  Then
+// the sums of max(P - Q, 0) over segments of the one row a sequence draws from, and the
+// draw itself from its segment; each of these works out the accepted tokens anew, a
+// lane a token, which is cheaper than a launch.
 #include "sample_row.h"
 
 namespace lora {
@@ -18,15 +19,16 @@ namespace lora {
 namespace {
 
 constexpr double kUnit = 1099511627776.0;    // 2^40, the probability 1
-constexpr int kSegment = 4096;               // columns of a segment
+constexpr int kSegment = 2048;               // columns of a segment
 constexpr int kSumThreads = 256;
 
 // What is left of a row once its cuts are known.
 struct Cut {
     uint64_t total;                          // kept weight, 0: every logit masked
     uint64_t last;                           // place of the last element kept, or a lower one
+    double given;                            // P or Q of the drafted token
     float lmax;
-    uint32_t pad[3];
+    uint32_t weight;                         // kept weight of the drafted token
 };
 
 __device__ __forceinline__ RowSettings settings_of(const VerifyParams& p, int64_t i)
@@ -35,15 +37,51 @@ __device__ __forceinline__ RowSettings settings_of(const VerifyParams& p, int64_
             p.min_p ? p.min_p[i] : 0.0f, 0.0f};
 }
 
+// A row's distribution.
+struct Dist {
+    Row r;
+    uint64_t total, last;
+    double unit;                             // 2^40 / total
+    uint32_t floor_w;
+    bool greedy;
+
+    // Kept weight of column i with logit l.
+    __device__ __forceinline__ uint32_t kept(float l, int i) const
+    {
+        const uint64_t at = place(order_key(l), i);
+        if (greedy)
+            return at == last && total ? 1u : 0u;
+        const uint32_t w = weight(r, l);
+        return w >= floor_w && at >= last && total ? w : 0u;
+    }
+    __device__ __forceinline__ double probability(uint32_t w) const { return rint((double)w * unit); }
+};
+
+__device__ __forceinline__ Dist dist_from(uint64_t total, uint64_t last, float lmax, const RowSettings& set)
+{
+    Dist d{};
+    set_inverse(d.r, set.temperature);
+    set_maximum(d.r, lmax);
+    d.total = total;
+    d.last = last;
+    d.unit = total ? kUnit / (double)total : 0.0;
+    d.floor_w = weight_floor(set.min_p);
+    d.greedy = !(set.temperature > 0.0f);
+    return d;
+}
+
 struct ToWorkspace {
     static constexpr bool kDraw = false;
     Cut* cut;
+    RowSettings set;
+    int x;                                   // the drafted token, -1: none
+    float logit_x;
 
     __device__ __forceinline__ void kept(float lmax, uint64_t total, uint64_t last) const
     {
-        cut->total = total;
-        cut->last = last;
-        cut->lmax = lmax;
+        const Dist d = dist_from(total, last, lmax, set);
+        const uint32_t w = x >= 0 ? d.kept(logit_x, x) : 0;
+        *cut = {total, last, d.probability(w), lmax, w};
     }
     __device__ __forceinline__ void first(uint64_t top) const { kept(0.0f, top ? 1 : 0, top); }
     __device__ __forceinline__ void none() const { kept(0.0f, 0, 0); }
@@ -69,47 +107,24 @@ __global__ void __launch_bounds__(kThreads) k_verify_rows(VerifyParams p)
     const int j = (int)(at - i * per), n = drafts_of(p, i);
     if (draft ? j >= n : j > n)              // behind the sequence's drafts
         return;
-    const char* base = static_cast<const char*>(draft ? p.draft : p.target);
-    sample_row<BF16>(ToWorkspace{static_cast<Cut*>(p.workspace) + row},
-                     base + at * (draft ? p.ld_d : p.ld_t) * (BF16 ? 2 : 4), p.V, settings_of(p, i), lds);
-}
-
-// A row's distribution.
-struct Dist {
     Row r;
-    uint64_t total, last;
-    double unit;                             // 2^40 / total
-    uint32_t floor_w;
-    bool greedy;
-
-    // Kept weight of column i with logit l.
-    __device__ __forceinline__ uint32_t kept(float l, int i) const
-    {
-        const uint64_t at = place(order_key(l), i);
-        if (greedy)
-            return at == last && total ? 1u : 0u;
-        const uint32_t w = weight(r, l);
-        return w >= floor_w && at >= last && total ? w : 0u;
-    }
-    __device__ __forceinline__ double probability(uint32_t w) const { return rint((double)w * unit); }
-};
+    r.logits = static_cast<const char*>(draft ? p.draft : p.target) + at * (draft ? p.ld_d : p.ld_t) * (BF16 ? 2 : 4);
+    r.bf16 = BF16;
+    const int x = j < n ? p.drafted[i * p.n + j] : -1;
+    const RowSettings set = settings_of(p, i);
+    sample_row<BF16>(ToWorkspace{static_cast<Cut*>(p.workspace) + row, set, x, x >= 0 ? logit(r, x) : 0.0f}, r.logits, p.V,
+                     set, lds);
+}
 
 __device__ __forceinline__ Dist dist_of(const VerifyParams& p, bool bf16, bool draft, int64_t i, int j,
                                         const RowSettings& set)
 {
     const int64_t at = draft ? i * p.n + j : i * (p.n + 1) + j;
     const Cut& cut = static_cast<const Cut*>(p.workspace)[draft ? p.B * (p.n + 1) + at : at];
-    Dist d;
+    Dist d = dist_from(cut.total, cut.last, cut.lmax, set);
     d.r.logits = static_cast<const char*>(draft ? p.draft : p.target) + at * (draft ? p.ld_d : p.ld_t) * (bf16 ? 2 : 4);
     d.r.bf16 = bf16;
     d.r.V = p.V;
-    set_inverse(d.r, set.temperature);
-    set_maximum(d.r, cut.lmax);
-    d.total = cut.total;
-    d.last = cut.last;
-    d.unit = cut.total ? kUnit / (double)cut.total : 0.0;
-    d.floor_w = weight_floor(set.min_p);
-    d.greedy = !(set.temperature > 0.0f);
     return d;
 }
 
@@ -124,25 +139,23 @@ __device__ __forceinline__ float log_of(uint32_t w, uint64_t total)
     return logf((float)((double)w / (double)total));
 }
 
-// The accepted tokens of sequence i; the whole wave, lane j tests x_j.
-__device__ __forceinline__ Verdict verdict_of(const VerifyParams& p, bool bf16, int64_t i, const RowSettings& set)
+// The accepted tokens of sequence i; the whole wave, lane j tests x_j.  All it reads is asked
+// for at once; what lies behind the drafts' end was not written and is not looked at.
+__device__ __forceinline__ Verdict verdict_of(const VerifyParams& p, int64_t i)
 {
-    const int lane = threadIdx.x & 63, n = drafts_of(p, i);
-    Verdict v{};
-    bool ok = false;
-    if (lane < n) {
-        const int x = p.drafted[i * p.n + lane];
-        const float u = p.u[i * (p.n + 1) + lane];
-        const Dist t = dist_of(p, bf16, false, i, lane, set);
-        const uint32_t w = t.kept(logit(t.r, x), x);
-        double q = kUnit;
-        if (p.draft) {
-            const Dist d = dist_of(p, bf16, true, i, lane, set);
-            q = d.probability(d.kept(logit(d.r, x), x));
-        }
-        ok = (u > 0.0f ? (double)u * q : 0.0) < t.probability(w);
-        v.logprob = log_of(w, t.total);
-    }
+    const int lane = threadIdx.x & 63;
+    const Cut* cuts = static_cast<const Cut*>(p.workspace);
+    const int j = min(lane, max(p.n - 1, 0));
+    const float u = p.u[i * (p.n + 1) + j];
+    const Cut& t = cuts[i * (p.n + 1) + j];
+    const double P = t.given;
+    const uint32_t w = t.weight;
+    const uint64_t total = t.total;
+    const double Q = p.draft ? cuts[p.B * (p.n + 1) + i * p.n + j].given : kUnit;
+    const int n = drafts_of(p, i);
+    const bool ok = lane < n && (u > 0.0f ? (double)u * Q : 0.0) < P;
+    Verdict v;
+    v.logprob = ok ? log_of(w, total) : 0.0f;
     v.accepted = __builtin_ctzll(~__ballot(ok));               // lane 63 tests nothing
     v.rejected = v.accepted < n;
     return v;
@@ -210,10 +223,10 @@ __global__ void __launch_bounds__(kSumThreads) k_verify_sums(VerifyParams p, int
     const int64_t i = blockIdx.x / (uint32_t)segs;
     const int seg = (int)(blockIdx.x % (uint32_t)segs), len = segment_length(p.V);
     const RowSettings set = settings_of(p, i);
-    const Source s = source_of(p, BF16, i, verdict_of(p, BF16, i, set), set);
+    const Source s = source_of(p, BF16, i, verdict_of(p, i), set);
     const int end = min(p.V, (seg + 1) * len);
     uint64_t sw = 0, sr = 0;
-#pragma unroll 4
+#pragma unroll 8
     for (int c = seg * len + threadIdx.x; c < end; c += kSumThreads) {
         uint32_t w;
         uint64_t rest;
@@ -246,7 +259,7 @@ __global__ void __launch_bounds__(kThreads) k_verify_draw(VerifyParams p, int se
     __shared__ int pick;
     const int64_t i = blockIdx.x;
     const RowSettings set = settings_of(p, i);
-    const Verdict v = verdict_of(p, BF16, i, set);
+    const Verdict v = verdict_of(p, i);
     const Source s = source_of(p, BF16, i, v, set);
     // sums of the segments, a thread each
     static_assert(kMaxSegments <= kThreads, "");

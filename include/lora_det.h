@@ -658,7 +658,7 @@ int lora_sample(const void* logits, int32_t logits_type, int64_t ld, int64_t B, 
  *   logprobs  fp32 [B][n + 1] or NULL: log(w_j(token) / W_j), -inf for -1
  * logits, settings and their defaults as for lora_sample (rows of both tensors have
  * the same type; settings are per sequence, [B]); drafted int32 [B][n], u fp32
- * [B][n + 1].  0 <= n <= 63, B (2n + 1) <= 2^21, B V < 2^35.
+ * [B][n + 1].  0 <= n <= 63, B (2n + 1) <= 2^21, B V < 2^34.
  * workspace: lora_verify_workspace_bytes(B, n) bytes, 16-byte aligned, no
  * initialisation needed.  Three launches.
  */
