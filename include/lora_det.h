@@ -736,10 +736,10 @@ typedef struct lora_kv_cache {
  * exceeds 448 * 2^(byte - 127) (246 where there is none; what exceeds it becomes the
  * largest code).  Tokens appended to a block that has earlier
  * ones keep its byte unless they need a larger one: then the earlier codes are
- * rounded to the new byte from the values they stand for.  (A first token in a block
- * begins it anew; what a step leaves in a block behind its last token is unspecified
- * only if nothing was ever written there.)  So what the cache holds depends on the
- * sequence's tokens and on where its steps begin, on nothing else.
+ * rounded to the new byte from the values they stand for.  A first token in a block
+ * begins it anew; codes behind a step's last token are left as they are.  So what the
+ * cache holds of a sequence depends on its tokens and on where its steps begin, on
+ * nothing else.
  * q, q_out: bf16 [T][ld], q_heads * D columns, or both NULL; q_out may be q with the
  * same leading dimension.  k, v: bf16 [T][ld], heads * D columns.
  * 16-byte aligned, leading dimensions multiples of 8 (of rope: 4); rope_dim a
@@ -769,8 +769,8 @@ int lora_kv_append(const lora_kv_cache* cache, const uint16_t* q, int64_t ld_q, 
  * new tokens and max_len tokens; a large batch runs best with few chunks.  A query's
  * bits depend on it, its sequence's cache, chunk and max_new's class
  * (max_new * q_heads / heads up to 16, up to 64, above) only.
- *   max_new   the longest run of new tokens: it picks the kernel, a longer one is
- *             served too
+ *   max_new   the longest run of new tokens: it picks the kernel; a longer one is
+ *             served too, but much more slowly if it is a prompt among single tokens
  *   max_len   the longest seq_lens (the grid is made for it; tokens behind are not
  *             seen).  At most 2^30, and taken as max_pages * page_size where that
  *             is less
