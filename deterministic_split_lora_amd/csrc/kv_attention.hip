@@ -17,8 +17,8 @@
 // bytes: 61 sequences of up to 16384, 64 heads, 280 us (4.6 TB/s; 250, 5.2 TB/s, in chunks
 // of 2048); one of 131071 48 us (5.5 TB/s, of which the last-level cache has a part; 58 when
 // it has none); one of 1025 9.5 (two launches); 32 x 5 drafts, heads of 64, 39.  Many rows,
-// by the matrix cores and the vector unit together: prompts of 8191 and 5119 tokens 805-828
-// us (920-950 TFLOP/s; a large library product of bf16 reaches 1450), 512 tokens against
+// by the matrix cores and the vector unit together: prompts of 8191 and 5119 tokens 805-862
+// us (890-950 TFLOP/s; a large library product of bf16 reaches 1450), 512 tokens against
 // 32768 303-320 (850-900).
 #include "kv_cache.h"
 
@@ -135,7 +135,7 @@ __global__ void __launch_bounds__(kWaves * 64, D * NT <= 128 ? 2 : 1) k_attentio
     constexpr int kLoads = D / 64;           // 16-byte loads of a key by its 4 lanes
     constexpr int kOut = D / 16;             // tiles of 16 d
     __shared__ float ml[kWaves][R][2];
-    __shared__ float ow[kWaves][16][D + 4];
+    __shared__ __align__(16) float ow[kWaves][16][D + 4];
     const int H = p.cache.heads, G = p.q_heads / H;
     const int lane = threadIdx.x & 63, li = lane & 15, g = lane >> 4;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -558,8 +558,9 @@ __global__ void __launch_bounds__(kWaves * 64, D == 256 ? 1 : 2) k_attention_til
         const float s = pow2_of_scale(kscale);
 #pragma unroll
         for (int j = 0; j < kPieces; ++j) {
-            lds.k[buf][k_piece + 4 * j][0][wave * kKvBlock + k_key] = __builtin_bit_cast(u32x4, widen(kr[j][0], kr[j][1], s));
-            lds.k[buf][k_piece + 4 * j][1][wave * kKvBlock + k_key] = __builtin_bit_cast(u32x4, widen(kr[j][2], kr[j][3], s));
+            auto& to = lds.k[buf][k_piece + 4 * j];
+            to[0][wave * kKvBlock + k_key] = __builtin_bit_cast(u32x4, widen(kr[j][0], kr[j][1], s));
+            to[1][wave * kKvBlock + k_key] = __builtin_bit_cast(u32x4, widen(kr[j][2], kr[j][3], s));
         }
     };
     // gaps: some rows do not see all keys of the step
