@@ -268,8 +268,8 @@ __global__ void __launch_bounds__(kWaves * 64, D * NT <= 128 ? 2 : 1) k_attentio
                             const bool in = !missing && key >= seen[n].lo && key <= seen[n].hi;
                             s[n][t][i] = in ? s[n][t][i] : -INFINITY;
                         }
-                // a block that was never written may hold anything, its scale too
-                const bool unseen = missing || pv > last.hi;
+                // a block that no row sees may hold anything, its scale too
+                const bool unseen = missing || pv > last.hi || pv + kKvBlock <= first.lo;
                 vs = unseen ? 1.0f : vs;
 #pragma unroll
                 for (int d = 0; d < kOut; ++d)
@@ -566,8 +566,9 @@ __global__ void __launch_bounds__(kWaves * 64, D == 256 ? 1 : 2) k_attention_til
     // gaps: some rows do not see all keys of the step
     auto store_v = [&](bool gaps, int buf, int step, int page) __attribute__((always_inline)) {
         if (gaps) {
-            // a block that was never written may hold anything, its scale too
-            const bool unseen = page < 0 || step * kKeys + wave * kKvBlock > last.hi;
+            // a block that no row sees may hold anything, its scale too
+            const int key = step * kKeys + wave * kKvBlock;
+            const bool unseen = page < 0 || key > last.hi || key + kKvBlock <= first.lo;
             vscale = unseen ? 127u : vscale;
 #pragma unroll
             for (int j = 0; j < kPieces; ++j) {
