@@ -5,13 +5,18 @@
 // of the group; a wave has tiles of 16 rows as the columns of its matrix products:
 //   S^T = K Q^T     a step's 64 keys x 16 rows, four products of 16 keys
 //   O^T += V^T P^T  D x 16 rows, reduced over the step's 64 keys
-// and keeps for each row the maximum m and the sum l of the softmax (base 2).
+// With e the exponent of a block's value scale, the weight of a key in the second is
+//   P = 2^(S + e - m),  m = max(S + e)      (base 2)
+// so V enters as its codes, exactly, in fp16, and P too: times 2^15, of 11 bits down to
+// 2^-29 of the largest, with steps of 2^-39 of it below.  (As bf16, with the scale in V,
+// P's 8 bits were the larger half of the output's error; prompts took 3-4% less time,
+// few rows the same.)  The sum of the softmax, l = sum 2^(S - m), is taken before that
+// rounding and in fp32, as m and O are.
 // Key rows are dealt to the products so that lane group g (16 lanes) gets the S
 // of the step's block g, all 16 tokens: these are the P it then supplies, and the
 // tokens of the 16 bytes of V that it loads.  No value changes lanes but for the
-// row's maximum and sum.  Codes become bf16 (exactly) on the way from the load to
-// the product, times their block's scale.  P enters the product with V as bf16 (half a
-// step, 2^-8 of each p), sums and outputs are fp32.
+// row's maximum and sum.  Codes of K become bf16 (exactly) on the way from the load to
+// the product, times their block's scale.
 //
 // Measured on MI355X, 8 key heads of 128 unless said otherwise.  Few rows, by the cache's
 // bytes: 61 sequences of up to 16384, 64 heads, 280 us (4.6 TB/s; 250, 5.2 TB/s, in chunks
@@ -34,7 +39,12 @@ constexpr int kWaves = 4;
 constexpr float kLog2e = 1.44269504088896340736f;
 constexpr float kLn2 = 0.69314718055994530942f;
 
+constexpr int kUp = 15;                      // P and O are held times 2^15
+constexpr float kDown = 1.0f / (1 << kUp);
+
 typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
+typedef _Float16 f16x2 __attribute__((ext_vector_type(2)));
+typedef _Float16 f16x8 __attribute__((ext_vector_type(8)));    // converted to nearest, ties to even
 
 // Eight codes times a power of two.
 __device__ __forceinline__ bf16x8 widen(uint32_t lo, uint32_t hi, float scale)
@@ -44,6 +54,28 @@ __device__ __forceinline__ bf16x8 widen(uint32_t lo, uint32_t hi, float scale)
     const bf16x2 c = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(hi, scale, false);
     const bf16x2 d = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(hi, scale, true);
     return bf16x8{a[0], a[1], b[0], b[1], c[0], c[1], d[0], d[1]};
+}
+
+// Eight codes, exactly.
+__device__ __forceinline__ f16x8 widen_f16(uint32_t lo, uint32_t hi)
+{
+    const f16x2 a = __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(lo, 1.0f, false);
+    const f16x2 b = __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(lo, 1.0f, true);
+    const f16x2 c = __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(hi, 1.0f, false);
+    const f16x2 d = __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(hi, 1.0f, true);
+    return f16x8{a[0], a[1], b[0], b[1], c[0], c[1], d[0], d[1]};
+}
+
+// A maximum large enough that no rounding of the exponents makes a P larger than 2^kUp.
+__device__ __forceinline__ float above(float m)
+{
+    return fmaf(fabsf(m), 0x1p-22f, m);      // NaN of -inf, which the next maximum drops
+}
+
+// What takes a sum of P of a block with this scale byte to its part of l.
+__device__ __forceinline__ float back_of(int byte)
+{
+    return __builtin_amdgcn_ldexpf(1.0f, 127 - kUp - byte);
 }
 
 // Of each byte that is a NaN code the top bit, of others 0.
@@ -163,7 +195,8 @@ __global__ void __launch_bounds__(kWaves * 64, D * NT <= 128 ? 2 : 1) k_attentio
         // this lane's row of the S products is a key of block li / 4, its V is of block g
         int page_k = -1, page_v = -1;            // of the step that is loaded next
         u32x4 kc[4][kLoads], vc[kOut];
-        float ks = 1.0f, vs = 1.0f;
+        float ks = 1.0f;
+        int vs = 127;                            // the scale byte of V's block
         auto pages_of = [&](int step) {
             page_k = kv_page(p.cache, w.b, (int64_t)step * kStep + li / 4 * kKvBlock);
             page_v = kv_page(p.cache, w.b, (int64_t)step * kStep + g * kKvBlock);
@@ -183,7 +216,7 @@ __global__ void __launch_bounds__(kWaves * 64, D * NT <= 128 ? 2 : 1) k_attentio
             const int64_t i = max(page_v, 0);
             const int at = head * P + ((step * kStep + g * kKvBlock) & (P - 1));
             const uint8_t* src = p.cache.v + i * p.cache.ld_v + (int64_t)at * D + 16 * li;
-            vs = pow2_of_scale(p.cache.v_scales[i * p.cache.ld_vs + at / kKvBlock]);
+            vs = p.cache.v_scales[i * p.cache.ld_vs + at / kKvBlock];
 #pragma unroll
             for (int d = 0; d < kOut; ++d)
                 vc[d] = *(const global_u32x4*)(src + 16 * 16 * d);
@@ -268,9 +301,8 @@ __global__ void __launch_bounds__(kWaves * 64, D * NT <= 128 ? 2 : 1) k_attentio
                             const bool in = !missing && key >= seen[n].lo && key <= seen[n].hi;
                             s[n][t][i] = in ? s[n][t][i] : -INFINITY;
                         }
-                // a block that no row sees may hold anything, its scale too
+                // a block that no row sees may hold anything
                 const bool unseen = missing || pv > last.hi || pv + kKvBlock <= first.lo;
-                vs = unseen ? 1.0f : vs;
 #pragma unroll
                 for (int d = 0; d < kOut; ++d)
 #pragma unroll
@@ -279,7 +311,8 @@ __global__ void __launch_bounds__(kWaves * 64, D * NT <= 128 ? 2 : 1) k_attentio
                         bad |= nan_bytes(vc[d][i]);
                     }
             }
-            bf16x8 prob[NT][2];
+            const float e = (float)(vs - 127), back = back_of(vs);
+            f16x8 prob[NT][2];
 #pragma unroll
             for (int n = 0; n < NT; ++n) {
                 float top = -INFINITY;
@@ -288,19 +321,19 @@ __global__ void __launch_bounds__(kWaves * 64, D * NT <= 128 ? 2 : 1) k_attentio
 #pragma unroll
                     for (int i = 0; i < 4; ++i)
                         top = fmaxf(top, s[n][t][i]);
-                const float mn = fmaxf(m[n], group_max(top) * sl);
-                const float shift = shift_of(mn), f = __builtin_amdgcn_exp2f(m[n] - shift);
+                const float mn = fmaxf(m[n], above(group_max(fmaf(top, sl, e))));
+                const float shift = shift_of(mn), up = e + (float)kUp - shift, f = __builtin_amdgcn_exp2f(m[n] - shift);
                 m[n] = mn;
                 float sum = 0.0f;
 #pragma unroll
                 for (int t = 0; t < 4; ++t)
 #pragma unroll
                     for (int i = 0; i < 4; ++i) {
-                        const float e = __builtin_amdgcn_exp2f(fmaf(s[n][t][i], sl, -shift));
-                        sum += e;
-                        prob[n][t / 2][4 * (t % 2) + i] = (__bf16)e;
+                        const float x = __builtin_amdgcn_exp2f(fmaf(s[n][t][i], sl, up));
+                        sum += x;
+                        prob[n][t / 2][4 * (t % 2) + i] = (_Float16)x;
                     }
-                l[n] = l[n] * f + sum;
+                l[n] = fmaf(sum, back, l[n] * f);
 #pragma unroll
                 for (int d = 0; d < kOut; ++d)
 #pragma unroll
@@ -343,11 +376,11 @@ __global__ void __launch_bounds__(kWaves * 64, D * NT <= 128 ? 2 : 1) k_attentio
             }
 #pragma unroll
             for (int d = 0; d < kOut; ++d) {
-                const bf16x8 v0 = widen(vc[d][0], vc[d][1], vs), v1 = widen(vc[d][2], vc[d][3], vs);
+                const f16x8 v0 = widen_f16(vc[d][0], vc[d][1]), v1 = widen_f16(vc[d][2], vc[d][3]);
 #pragma unroll
                 for (int n = 0; n < NT; ++n) {
-                    o[n][d] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(v0, prob[n][0], o[n][d], 0, 0, 0);
-                    o[n][d] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(v1, prob[n][1], o[n][d], 0, 0, 0);
+                    o[n][d] = __builtin_amdgcn_mfma_f32_16x16x32_f16(v0, prob[n][0], o[n][d], 0, 0, 0);
+                    o[n][d] = __builtin_amdgcn_mfma_f32_16x16x32_f16(v1, prob[n][1], o[n][d], 0, 0, 0);
                 }
             }
             if (more)
@@ -396,7 +429,7 @@ __global__ void __launch_bounds__(kWaves * 64, D * NT <= 128 ? 2 : 1) k_attentio
                         const f32x4 y = *reinterpret_cast<const f32x4*>(&ow[v][r][c + c0]);
 #pragma unroll
                         for (int i = 0; i < 4; ++i)
-                            x[i] += y[i] * f[v];
+                            x[i] += y[i] * (f[v] * kDown);
                     }
                     if (several) {
                         float* dst = p.partial + ((chunk * p.T + at) * p.q_heads + h) * partial_floats(D);
@@ -417,7 +450,7 @@ __global__ void __launch_bounds__(kWaves * 64, D * NT <= 128 ? 2 : 1) k_attentio
 
 // ---------------------------------------------------------------------------
 // Many rows (prompts): bound by the matrix cores.  A workgroup has 128 rows, a wave
-// 32 of them; K and V of a step are widened to bf16 on their way to LDS, once for
+// 32 of them; K and V of a step are widened to 16 bits on their way to LDS, once for
 // all waves, and lie there in the order of the operands:
 //   S^T = K Q^T       32x32x16 products, 32 keys x 32 rows
 //   O^T += V^T P^T    32x32x16 products, 32 d x 32 rows
@@ -435,7 +468,8 @@ constexpr int kTileRows = kWaves * 32;
 template <int D>
 struct TileLds {
     u32x4 k[2][D / 16][2][kStep];            // bf16: 8 d of a key, for each lane half
-    u32x4 v[2][kStep / kKvBlock][2][D];      // bf16: 8 keys of a d, for each lane half
+    u32x4 v[2][kStep / kKvBlock][2][D];      // fp16: 8 keys of a d, for each lane half
+    int v_exponent[2][kStep / kKvBlock];     // of the blocks' scales, written with K
     uint32_t nan_step[2];                    // the last step with a value that is NaN
     uint16_t nan[2][kStep / kKvBlock][D];    // then: which keys' value of a d is
 };
@@ -544,6 +578,7 @@ __global__ void __launch_bounds__(kWaves * 64, D == 256 ? 1 : 2) k_attention_til
         for (int j = 0; j < kPieces; ++j)
             kr[j] = *(const global_u32x4*)(src + (k_key * D + 16 * k_piece + 64 * j));
         kscale = p.cache.k_scales[g * p.cache.ld_ks + at / kKvBlock];
+        vscale = p.cache.v_scales[g * p.cache.ld_vs + at / kKvBlock];
     };
     auto load_v = [&](int step, int page) __attribute__((always_inline)) {
         const int64_t g = max(page, 0);
@@ -552,10 +587,10 @@ __global__ void __launch_bounds__(kWaves * 64, D == 256 ? 1 : 2) k_attention_til
 #pragma unroll
         for (int j = 0; j < kPieces; ++j)
             vr[j] = *(const global_u32x4*)(src + (lane * 16 + 1024 * j));
-        vscale = p.cache.v_scales[g * p.cache.ld_vs + at / kKvBlock];
     };
     auto store_k = [&](int buf) __attribute__((always_inline)) {
         const float s = pow2_of_scale(kscale);
+        lds.v_exponent[buf][wave] = (int)vscale - 127;
 #pragma unroll
         for (int j = 0; j < kPieces; ++j) {
             auto& to = lds.k[buf][k_piece + 4 * j];
@@ -566,10 +601,9 @@ __global__ void __launch_bounds__(kWaves * 64, D == 256 ? 1 : 2) k_attention_til
     // gaps: some rows do not see all keys of the step
     auto store_v = [&](bool gaps, int buf, int step, int page) __attribute__((always_inline)) {
         if (gaps) {
-            // a block that no row sees may hold anything, its scale too
+            // a block that no row sees may hold anything
             const int key = step * kKeys + wave * kKvBlock;
             const bool unseen = page < 0 || key > last.hi || key + kKvBlock <= first.lo;
-            vscale = unseen ? 127u : vscale;
 #pragma unroll
             for (int j = 0; j < kPieces; ++j) {
                 uint32_t bad = 0;
@@ -584,16 +618,15 @@ __global__ void __launch_bounds__(kWaves * 64, D == 256 ? 1 : 2) k_attention_til
                     lds.nan_step[buf] = (uint32_t)step;
             }
         }
-        const float s = pow2_of_scale(vscale);
 #pragma unroll
         for (int j = 0; j < kPieces; ++j) {
-            lds.v[buf][wave][0][lane + 64 * j] = __builtin_bit_cast(u32x4, widen(vr[j][0], vr[j][2], s));
-            lds.v[buf][wave][1][lane + 64 * j] = __builtin_bit_cast(u32x4, widen(vr[j][1], vr[j][3], s));
+            lds.v[buf][wave][0][lane + 64 * j] = __builtin_bit_cast(u32x4, widen_f16(vr[j][0], vr[j][2]));
+            lds.v[buf][wave][1][lane + 64 * j] = __builtin_bit_cast(u32x4, widen_f16(vr[j][1], vr[j][3]));
         }
     };
 
     typedef f32x16 Logits[kTiles];
-    typedef bf16x8 Probs[kBlocks];
+    typedef f16x8 Probs[kBlocks];
     auto product = [&](int buf, Logits& out) __attribute__((always_inline)) {
 #pragma unroll
         for (int t = 0; t < kTiles; ++t)
@@ -611,8 +644,8 @@ __global__ void __launch_bounds__(kWaves * 64, D == 256 ? 1 : 2) k_attention_til
         for (int u = 0; u < kBlocks; ++u)
 #pragma unroll
             for (int d = 0; d < kOut; ++d) {
-                const bf16x8 v = __builtin_bit_cast(bf16x8, lds.v[buf][u][h][32 * d + r]);
-                o[d] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(v, prob[u], o[d], 0, 0, 0);
+                const f16x8 v = __builtin_bit_cast(f16x8, lds.v[buf][u][h][32 * d + r]);
+                o[d] = __builtin_amdgcn_mfma_f32_32x32x16_f16(v, prob[u], o[d], 0, 0, 0);
             }
     };
     // a value that is NaN reaches the rows that see its key, and no others
@@ -635,6 +668,12 @@ __global__ void __launch_bounds__(kWaves * 64, D == 256 ? 1 : 2) k_attention_til
     const int s0 = (int)(begin / kKeys), s1 = (int)((end + kKeys - 1) / kKeys);
     int page_v = -1, page_k = -1;            // of the next step, the one behind it
     uint32_t gone = 0, gone_next = 0, gone_far = 0;    // of this step, the next, the one behind it
+    int e[kBlocks];                          // exponents of the step's V, the same in every lane
+    auto exponents = [&](int buf) __attribute__((always_inline)) {
+#pragma unroll
+        for (int u = 0; u < kBlocks; ++u)
+            e[u] = __builtin_amdgcn_readfirstlane(lds.v_exponent[buf][u]);
+    };
     Logits s_even, s_odd;                    // of the even and odd steps from the first on
     if (threadIdx.x < 2)
         lds.nan_step[threadIdx.x] = 0xFFFFFFFFu;
@@ -653,6 +692,7 @@ __global__ void __launch_bounds__(kWaves * 64, D == 256 ? 1 : 2) k_attention_til
         load_k(s0 + 2, page_k);
         __syncthreads();
         product(s0 & 1, s_even);
+        exponents(s0 & 1);
         __syncthreads();                     // K of the first step is read: its place is free
     }
     // One step: its S are in s, those of the next go to s_next.  V of the next step and K of the
@@ -671,13 +711,17 @@ __global__ void __launch_bounds__(kWaves * 64, D == 256 ? 1 : 2) k_attention_til
                     s[t][i] = sees ? s[t][i] : -INFINITY;
                 }
         }
-        float top = -INFINITY;
+        float top;
 #pragma unroll
-        for (int t = 0; t < kTiles; ++t)
+        for (int u = 0; u < kBlocks; ++u) {
+            float of_block = s[u / 2][u % 2 * 8];
 #pragma unroll
-            for (int i = 0; i < 16; ++i)
-                top = fmaxf(top, s[t][i]);
-        const float mn = fmaxf(m, half_max(top) * sl);
+            for (int i = 1; i < 8; ++i)
+                of_block = fmaxf(of_block, s[u / 2][u % 2 * 8 + i]);
+            const float scaled = fmaf(of_block, sl, (float)e[u]);
+            top = u ? fmaxf(top, scaled) : scaled;
+        }
+        const float mn = fmaxf(m, above(half_max(top)));
         if (__any(mn > m)) {
             const float f = __builtin_amdgcn_exp2f(m - shift_of(mn));
             l *= f;
@@ -688,22 +732,24 @@ __global__ void __launch_bounds__(kWaves * 64, D == 256 ? 1 : 2) k_attention_til
                 for (int i = 0; i < 16; ++i)
                     o[d][i] *= f;
         }
-        const float shift = shift_of(m);
+        const float shift = shift_of(m) - (float)kUp;
         // a wave with products to give comes before the others' vector work: 820 -> 805 us
         // for prompts of 8191 and 5119 tokens, 32 heads
         __builtin_amdgcn_s_setprio(1);
         product(buf ^ 1, s_next);
         Probs prob;
-        float sum = 0.0f;                    // of the P before their rounding, which lse would show
 #pragma unroll
-        for (int t = 0; t < kTiles; ++t)
+        for (int u = 0; u < kBlocks; ++u) {
+            const float up = (float)e[u] - shift;
+            float sum = 0.0f;                // of the P before their rounding, which lse would show
 #pragma unroll
-            for (int i = 0; i < 16; ++i) {
-                const float x = __builtin_amdgcn_exp2f(fmaf(s[t][i], sl, -shift));
-                sum += x;
-                prob[2 * t + i / 8][i % 8] = (__bf16)x;
+            for (int i = 0; i < 8; ++i) {
+                const float x = __builtin_amdgcn_exp2f(fmaf(s[u / 2][u % 2 * 8 + i], sl, up));
+                sum = i ? sum + x : x;
+                prob[u][i] = (_Float16)x;
             }
-        l += sum;
+            l += __builtin_amdgcn_ldexpf(sum, -kUp - e[u]);
+        }
         store_k(buf);
         output(buf, prob);
         __builtin_amdgcn_s_setprio(0);
@@ -716,6 +762,7 @@ __global__ void __launch_bounds__(kWaves * 64, D == 256 ? 1 : 2) k_attention_til
         gone_next = gone_far;
         page_k = page_at(step + 3, gone_far);
         load_k(step + 3, page_k);
+        exponents(buf ^ 1);                  // K of the next step is there, and they with it
         __syncthreads();
     };
     // two steps a turn, so that nothing moves from the registers of a step to those of another
@@ -738,7 +785,7 @@ __global__ void __launch_bounds__(kWaves * 64, D == 256 ? 1 : 2) k_attention_til
     for (int d = 0; d < kOut; ++d)
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-            const f32x4 x = {o[d][4 * i], o[d][4 * i + 1], o[d][4 * i + 2], o[d][4 * i + 3]};
+            const f32x4 x = {o[d][4 * i] * kDown, o[d][4 * i + 1] * kDown, o[d][4 * i + 2] * kDown, o[d][4 * i + 3] * kDown};
             const int c = 32 * d + 8 * i + 4 * h;
             if (several)
                 *reinterpret_cast<f32x4*>(dst + 4 + c) = x;

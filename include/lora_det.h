@@ -761,8 +761,10 @@ int lora_kv_append(const lora_kv_cache* cache, const uint16_t* q, int64_t ld_q, 
  * A query that sees nothing gets 0 and -inf.  A NaN or an infinity in a key or value
  * that it does not see does not reach it.
  * Products are exact with fp32 accumulators; maximum, sum and output are held in
- * fp32, the p_j enter the product with v rounded to bf16 (relative to the largest of
- * the keys up to there).
+ * fp32.  A p_j, times the scale of its value's block, enters the product with v rounded
+ * to fp16 (half a step, 2^-11 of it; where it is below 2^-29 of the largest of these up
+ * to there, half a step is 2^-40 of that one).  Value scales of a sequence's head that
+ * lie more than 2^100 apart can lose the p_j of the smaller ones.
  * Keys are cut into chunks of `chunk` positions, [0, chunk), [chunk, 2 chunk), ..,
  * which run in parallel and are joined in ascending order in fp32.  chunk: a multiple
  * of 256, or 0 for lora_kv_attention_chunk's, which suits one sequence with max_new

@@ -3,7 +3,8 @@ tiles of them, many) with windows, pages that are not there, blocks that were ne
 import numpy as np
 import pytest
 
-from tests.helpers import gpu_available, torch
+from oracle import bf16_to_f64, kv
+from tests.helpers import bf16_from_gpu, gpu_available, torch
 from tests.kv_helpers import Batch, attend, heads_bf16
 
 pytestmark = [pytest.mark.gpu,
@@ -37,3 +38,41 @@ def test_blocks_before_the_window_may_hold_anything(D, P, new):
             out, lse = attend(qg, batch.gpu(), new, window=window)
             assert not bool(t.isnan(out).any()), (scale, code)
             assert t.equal(bits(out), bits(want)) and t.equal(bits(lse), bits(wlse)), (scale, code)
+
+
+@pytest.mark.parametrize("D", [64, 128, 256])
+@pytest.mark.parametrize("new", NEW)
+def test_weights_keep_eleven_bits(D, new):
+    """The bounds of oracle/kv.py with 2^-11 in the place of 2^-8 for the p (fp16, half a step), and for what is below
+    2^-29 of the largest half a step of 2^-39 of it, times codes up to 448, for every key: 448 2^-40 < 2^-31."""
+    batch = Batch([(new, 60), (new, 45)], 16, 1, D, seed=7).fill()
+    q, qg = heads_bf16(batch.T, 8, D, 1.0, 4, "q")
+    args = (batch.table, batch.lens, batch.cu, 16, D ** -0.5)
+    out, _, tol, _ = kv.attention(q, batch.cache, *args)
+    size = kv.attention(q, dict(batch.cache, v=batch.cache["v"] & 127), *args)[0]       # sums of p |v|
+    used = batch.cache["vs"][batch.table[batch.table >= 0]].max()
+    tol = tol - size * (2.0 ** -8 - 2.0 ** -11) + 60 * 2.0 ** (int(used) - 127 - 31)
+    for chunk in (0, 256):
+        got = bf16_to_f64(bf16_from_gpu(attend(qg, batch.gpu(), new, chunk=chunk)[0]))
+        assert np.all(np.abs(got - out) <= tol), np.max(np.abs(got - out) / tol)
+
+
+@pytest.mark.parametrize("new", NEW)
+def test_largest_values_and_zeros(new):
+    """Values at the top of bf16, whose sums would pass the largest float; a long run of zeros, whose scale is the least."""
+    t = torch()
+    batch = Batch([(new, 20000), (new, 300)], 128, 1, 64, seed=7)
+    batch.cache["k"][:] = 0
+    batch.cache["ks"][:] = 127
+    batch.cache["v"][:], batch.cache["vs"][:] = 0, 27
+    for page in batch.table[1][batch.table[1] >= 0]:
+        batch.cache["v"][page], batch.cache["vs"][page] = 0x7E, 246
+    q, qg = heads_bf16(batch.T, 8, 64, 1.0, 4, "q")
+    for chunk in (0, 1 << 20):
+        out, lse = attend(qg, batch.gpu(), new, chunk=chunk)
+        o = bf16_to_f64(bf16_from_gpu(out))
+        assert not o[:new].any()
+        assert np.all(np.abs(o[new:] / 2.0 ** 127 - 1.75) <= 1.75 * 2.0 ** -8)
+        # sums of equal numbers in fp32, and the size of what the scale's exponent adds to the logarithm
+        want = np.log(np.concatenate([np.arange(20000 - new, 20000), np.arange(300 - new, 300)]) + 1.0)
+        assert np.all(np.abs(lse.double().cpu().numpy() - want[:, None]) <= 2.0 ** -16)
