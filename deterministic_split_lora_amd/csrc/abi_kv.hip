@@ -96,6 +96,16 @@ int check_attention_sizes(int64_t T, int32_t q_heads, int32_t heads, int32_t D, 
     return LORA_OK;
 }
 
+// The chunk of a step whose sizes are sound: the default for 0, and no longer than the
+// caller's max_len needs, so that sums of both stay small.
+int64_t chunk_of(int64_t chunk, int64_t max_new, int32_t q_heads, int32_t heads, int32_t D, int64_t max_len)
+{
+    if (chunk == 0)
+        return kv_attention_chunk(max_new, q_heads, heads, D, max_len);
+    const int64_t whole = (max_len + kKvChunkUnit - 1) / kKvChunkUnit * kKvChunkUnit;
+    return chunk < whole ? chunk : whole;
+}
+
 }  // namespace
 
 extern "C" {
@@ -169,8 +179,7 @@ size_t lora_kv_attention_workspace_bytes(int64_t T, int32_t q_heads, int32_t hea
 {
     if (check_attention_sizes(T, q_heads, heads, head_dim, max_new, max_len, chunk) != LORA_OK || T == 0)
         return 0;
-    if (chunk == 0)
-        chunk = kv_attention_chunk(max_new, q_heads, heads, head_dim, max_len);
+    chunk = chunk_of(chunk, max_new, q_heads, heads, head_dim, max_len);
     if (max_len <= chunk)
         return 0;
     if (T * q_heads > kMaxThreads / kWaveGroup || T * q_heads * ((max_len + chunk - 1) / chunk) > kMaxThreads)
@@ -204,8 +213,7 @@ int lora_kv_attention(const lora_kv_cache* cache, const uint16_t* q, int64_t ld_
         return LORA_ERR_SHAPE;
     if (!aligned(q, 16) || !aligned(out, 16) || !aligned(lse, 4) || !aligned(workspace, 16) || ld_q % 8 || ld_out % 8)
         return LORA_ERR_ALIGN;
-    if (chunk == 0)                          // by the caller's max_len, as the workspace's size
-        chunk = kv_attention_chunk(max_new, q_heads, H, D, max_len);
+    chunk = chunk_of(chunk, max_new, q_heads, H, D, max_len);    // by the caller's max_len, as the workspace's size
     const int64_t capacity = cache->max_pages * cache->page_size;
     max_len = max_len < capacity ? max_len : capacity;
     if (kv_attention_blocks(T, cache->n_seqs, max_new, q_heads, H, D, max_len, chunk) > kMaxThreads / kWaveGroup ||

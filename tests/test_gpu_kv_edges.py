@@ -76,3 +76,15 @@ def test_largest_values_and_zeros(new):
         # sums of equal numbers in fp32, and the size of what the scale's exponent adds to the logarithm
         want = np.log(np.concatenate([np.arange(20000 - new, 20000), np.arange(300 - new, 300)]) + 1.0)
         assert np.all(np.abs(lse.double().cpu().numpy() - want[:, None]) <= 2.0 ** -16)
+
+
+@pytest.mark.parametrize("new", NEW)
+def test_the_longest_chunk(new):
+    """A chunk past every length, up to the largest number, is one chunk of the whole."""
+    t = torch()
+    batch = Batch([(new, 700), (new, 90)], 16, 1, 64, seed=7).fill()
+    q, qg = heads_bf16(batch.T, 8, 64, 1.0, 4, "q")
+    want, wlse = attend(qg, batch.gpu(), new, chunk=768)
+    for chunk in (1 << 31, (1 << 63) - 256):
+        out, lse = attend(qg, batch.gpu(), new, chunk=chunk)
+        assert t.equal(bits(out), bits(want)) and t.equal(bits(lse), bits(wlse))
