@@ -122,8 +122,8 @@ int lora_kv_append(const lora_kv_cache* cache, const uint16_t* q, int64_t ld_q, 
     const int64_t D = cache->head_dim;
     if (T < 0 || T > kMaxDim || (q && (q_heads < 1 || q_heads > kMaxHeads)))
         return LORA_ERR_SHAPE;
-    if ((pairs != 0 && pairs != 1) || (rope && (rope_dim < 16 || rope_dim > D || rope_dim % 16)) || (!q && q_norm) ||
-        (!q != !q_out))
+    if ((pairs != 0 && pairs != 1) || (rope && (rope_dim < 16 || rope_dim > D || rope_dim % 16)) ||
+        (T > 0 && !q && q_norm) || (!q != !q_out))
         return LORA_ERR_UNSUPPORTED;
     const int64_t blocks = (T / kKvBlock + 2 * cache->n_seqs) * cache->heads + (q ? T : 0);
     if (blocks * 2 * D > kMaxThreads)

@@ -3,6 +3,7 @@ tiles of them, many) with windows, pages that are not there, blocks that were ne
 import numpy as np
 import pytest
 
+import deterministic_split_lora_amd as dsl
 from oracle import bf16_to_f64, kv
 from tests.helpers import bf16_from_gpu, gpu_available, torch
 from tests.kv_helpers import Batch, attend, heads_bf16
@@ -88,3 +89,18 @@ def test_the_longest_chunk(new):
     for chunk in (1 << 31, (1 << 63) - 256):
         out, lse = attend(qg, batch.gpu(), new, chunk=chunk)
         assert t.equal(bits(out), bits(want)) and t.equal(bits(lse), bits(wlse))
+
+
+def test_a_step_without_tokens():
+    """Every argument of a step given, and no row in any of them."""
+    t = torch()
+    batch = Batch([(0, 20), (0, 5)], 16, 2, 64, seed=7).fill()
+    g = batch.gpu()
+    x = t.empty(0, 8, 64, dtype=t.bfloat16, device="cuda")
+    norm = t.ones(64, dtype=t.bfloat16, device="cuda")
+    rope = t.zeros(30, 64, device="cuda")
+    out = t.empty(0, 4, 64, dtype=t.bfloat16, device="cuda")
+    dsl.lora_kv_append(x[:, 4:6], x[:, 6:], g, q=x[:, :4], q_out=out, q_norm=norm, k_norm=norm, rope=rope)
+    dsl.lora_kv_attention(out, g, t.empty_like(out), 1, max_len=20, lse=t.empty(0, 4, device="cuda"))
+    t.cuda.synchronize()
+    batch.same(g)

@@ -3,7 +3,7 @@ import pytest
 
 import deterministic_split_lora_amd as dsl
 from deterministic_split_lora_amd import _binding as B
-from tests.test_kv_cpu import FAKE, attention, cache
+from tests.test_kv_cpu import FAKE, append, attention, cache
 
 LARGEST_CHUNK = (1 << 63) - 256
 
@@ -18,3 +18,10 @@ def test_any_chunk_of_the_length_or_more_is_one(chunk):
         assert attention(many, chunk=chunk, max_len=max_len, **huge) == B.LORA_ERR_SHAPE
         assert dsl.lora_kv_attention_workspace_bytes(4, 8, 2, 128, 1, max_len, chunk) == 0
     assert attention(chunk=chunk, ws=None, wsb=0, lse=None, ld_lse=0, out=FAKE + 2) == B.LORA_ERR_ALIGN
+
+
+def test_a_step_without_tokens():
+    """Tensors without elements have no address; the norm's weights are there all the same."""
+    assert append(T=0, q=None, q_out=None, k=None, v=None) == B.LORA_OK
+    assert append(T=0, q=None, q_out=None, k=None, v=None, rope_dim=8) == B.LORA_ERR_UNSUPPORTED
+    assert append(T=1, q=None, q_out=None) == B.LORA_ERR_UNSUPPORTED
