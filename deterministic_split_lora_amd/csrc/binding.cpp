@@ -427,6 +427,8 @@ PyObject* kv_append(PyObject*, PyObject* const* a, Py_ssize_t n)
                 refuse(PyExc_ValueError, "q and q_out must have the same heads");
         }
         const Matrix rope = matrix(a[8], at::kFloat, "rope", true);
+        if (a[8] != Py_None && rope.rows == 0)                 // without an address: no rotation
+            refuse(PyExc_ValueError, "rope must have rows");
         const int64_t ld_rope = rope.rows > 1 ? rope.ld : rope.cols;
         return kv_append_fn(&c, u16(q.p), q.ld, u16(q_out.p), q_out.ld, narrow(q.heads), u16(k.p), k.ld, u16(v.p),
                             v.ld, k.T, u16(vector(a[5], D, kBf16, "q_norm")), u16(vector(a[6], D, kBf16, "k_norm")),

@@ -104,3 +104,11 @@ def test_a_step_without_tokens():
     dsl.lora_kv_attention(out, g, t.empty_like(out), 1, max_len=20, lse=t.empty(0, 4, device="cuda"))
     t.cuda.synchronize()
     batch.same(g)
+
+
+def test_a_rotation_table_without_rows_is_refused():
+    t = torch()
+    g = Batch([(2, 20)], 16, 2, 64, seed=7).fill().gpu()
+    x = t.zeros(2, 4, 64, dtype=t.bfloat16, device="cuda")
+    with pytest.raises(ValueError, match="rope"):
+        dsl.lora_kv_append(x[:, :2], x[:, 2:], g, rope=t.empty(0, 64, device="cuda"))
