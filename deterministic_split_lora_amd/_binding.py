@@ -702,7 +702,8 @@ def lora_kv_append(k, v, cache, q=None, q_out=None, q_norm=None, k_norm=None, ro
                    eps: float = 1e-6, stream=None):
     """Appends the new tokens' keys and values ([T, heads, D] bf16, also views of a fused projection's output) to the
     cache, the keys normed per head (k_norm [D]) and rotated by their position (rope [positions, rope_dim] fp32: cosines,
-    then sines; pairs: neighbours rotate, not halves); q_out = q normed and rotated."""
+    then sines; pairs: neighbours rotate, not halves); q_out = q normed and rotated.  A block of 16 tokens shares a scale,
+    which later tokens of it can raise, also ones that are taken back afterwards (include/lora_det.h)."""
     st = (_native_module or _native()).kv_append(k, v, cache, q, q_out, q_norm, k_norm, eps, rope, pairs,
                                                  _stream_address(stream, k))
     if st:

@@ -8,7 +8,8 @@
 // largest value of the block's tokens is no more than 448.  A block that goes on
 // keeps its exponent unless the new tokens need a larger one; then its earlier
 // codes are rounded again, in place.  (A power of two: their exponent moves, and
-// only codes that become subnormal lose anything.)
+// only codes that become subnormal lose anything.)  It does not fall again when the
+// tokens that raised it are taken back: what their codes were is not kept.
 //
 // Every fp32 operation rounds on its own and the sum of squares is taken in fp64,
 // where its order leaves no trace: which code a value gets does not depend on how

@@ -135,7 +135,8 @@ def run(a):
     line = torch.randint(0, a.vocab, (B, n + 1), generator=gen, device="cuda", dtype=torch.int32)
     lengths = [p + n + 1 for p in a.prompts]
     first = step(model, caches, line.flatten(), [n + 1] * B, lengths, rope)
-    # half of the drafts are what the model itself would say; a token's logits do not depend on the drafts behind it
+    # each first draft is what the model itself would say (the drafts behind a token reach its logits only through the
+    # scale that their block of 16 tokens shares)
     own = first.view(B, n + 1, -1)[:, :n].float().argmax(-1).to(torch.int32)
     line[:, 1:2] = own[:, :1]
     logits = step(model, caches, line.flatten(), [n + 1] * B, lengths, rope)

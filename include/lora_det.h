@@ -651,6 +651,8 @@ int lora_sample(const void* logits, int32_t logits_type, int64_t ld, int64_t B, 
  *     everywhere); where the drafts ended, from w_a, as lora_sample draws:
  *     with S the sum of these numbers, the lowest index whose sum of the numbers up
  *     to it exceeds t = floor(u S) (at most S - 1)
+ * (Over a cache of lora_kv_append row j can hold a trace of the drafts behind x_{j-1}: the
+ * scale of a block is that of all its tokens.)
  * Greedy rows (temperature <= 0 or NaN) have weight 1 at their first token.  A row of
  * -inf only gives the token -1.
  *   tokens    int32 [B][n + 1]: the accepted ones, the drawn one, then -1
@@ -737,9 +739,13 @@ typedef struct lora_kv_cache {
  * largest code).  Tokens appended to a block that has earlier
  * ones keep its byte unless they need a larger one: then the earlier codes are
  * rounded to the new byte from the values they stand for.  A first token in a block
- * begins it anew; codes behind a step's last token are left as they are.  So what the
- * cache holds of a sequence depends on its tokens and on where its steps begin, on
- * nothing else.
+ * begins it anew; codes behind a step's last token are left as they are.
+ * So what the cache holds of a token depends on it, on the other tokens of its block
+ * (later ones too, of its own step among them), on where the sequence's steps begin, and
+ * on tokens of the block that were taken back since (a smaller seq_lens in a later call,
+ * as after rejected drafts): their byte stays, and codes that were rounded to it stay
+ * so.  It does not depend on other sequences.  Whoever needs the block as it was
+ * before a draft copies it (16 tokens of a head: 32 head_dim + 2 bytes) and puts it back.
  * q, q_out: bf16 [T][ld], q_heads * D columns, or both NULL; q_out may be q with the
  * same leading dimension.  k, v: bf16 [T][ld], heads * D columns.
  * 16-byte aligned, leading dimensions multiples of 8 (of rope: 4); rope_dim a

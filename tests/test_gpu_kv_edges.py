@@ -112,3 +112,31 @@ def test_a_rotation_table_without_rows_is_refused():
     x = t.zeros(2, 4, 64, dtype=t.bfloat16, device="cuda")
     with pytest.raises(ValueError, match="rope"):
         dsl.lora_kv_append(x[:, :2], x[:, 2:], g, rope=t.empty(0, 64, device="cuda"))
+
+
+@pytest.mark.parametrize("D", [64, 128, 256])
+def test_drafts_that_are_taken_back(D):
+    """A prompt, a token with drafts behind it of which one has values 200 times as large, and tokens that go on from the
+    accepted one: the same as the reference, whose byte stays raised."""
+    batch = Batch([(1, 40), (1, 40)], 32, 2, D, seed=7)
+    g = None
+    plain = None
+    for i, (new, lens) in enumerate([((20, 4), (20, 4)), ((3, 4), (23, 8)), ((1, 2), (22, 7)), ((1, 1), (23, 8))]):
+        batch.lens = np.array(lens, dtype=np.int32)
+        batch.cu = np.concatenate([[0], np.cumsum(new)]).astype(np.int32)
+        batch.T = int(batch.cu[-1])
+        x, xg = heads_bf16(batch.T, 4, D, 1.0, i, "x")
+        if i == 1:
+            plain = batch.cache["ks"][batch.table[:, 0]].copy(), batch.cache["vs"][batch.table[:, 0]].copy()
+            scale = np.ones(batch.T)
+            scale[[2, 5]] = 256.0                               # drafts: the second of the one, the second of the other
+            x = x * scale[:, None, None]
+            xg = (xg.float() * torch().from_numpy(scale).float().cuda()[:, None, None]).to(torch().bfloat16)
+        g = batch.gpu()
+        dsl.lora_kv_append(xg[:, :2], xg[:, 2:], g)
+        torch().cuda.synchronize()
+        kv.append(batch.cache, x[:, :2], x[:, 2:], batch.table, batch.lens, batch.cu, 32)
+        batch.same(g)
+    for name, old in zip(("ks", "vs"), plain):
+        now = batch.cache[name][batch.table[:, 0]]
+        assert np.all(now[0, :, 1] > old[0, :, 1] + 5) and np.all(now[1, :, 0] > old[1, :, 0] + 5)
