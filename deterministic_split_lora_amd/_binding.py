@@ -726,7 +726,8 @@ def lora_kv_attention(q, cache, out, max_new: int, max_len=None, scale=None, cau
     """out = attention of q ([T, q_heads, D] bf16) over the cache, lse = its log-sum-exp ([T, q_heads] fp32).  max_new,
     max_len: the longest run of new tokens and the longest sequence (default: all that the table holds); scale: default
     1 / sqrt(D); chunk: keys that one workgroup joins on its own (0: by these sizes); workspace: tensor of
-    lora_kv_attention_workspace_bytes, None if that is 0."""
+    lora_kv_attention_workspace_bytes, None if that is 0.  A sequence's bits do not depend on the others of its step where
+    chunk is named and max_new * q_heads / heads stays up to 16, up to 64, or above."""
     st = (_native_module or _native()).kv_attention(q, cache, out, max_new, max_len, scale, causal, window, chunk, lse,
                                                     workspace, _stream_address(stream, q))
     if st:

@@ -776,7 +776,9 @@ int lora_kv_append(const lora_kv_cache* cache, const uint16_t* q, int64_t ld_q, 
  * of 256, or 0 for lora_kv_attention_chunk's, which suits one sequence with max_new
  * new tokens and max_len tokens; a large batch runs best with few chunks.  A query's
  * bits depend on it, its sequence's cache, chunk and max_new's class
- * (max_new * q_heads / heads up to 16, up to 64, above) only.
+ * (max_new * q_heads / heads up to 16, up to 64, above) only.  The default chunk is
+ * another one where max_new or max_len is: a caller whose bits may not depend on the
+ * step's other sequences names one.
  *   max_new   the longest run of new tokens: it picks the kernel; a longer one is
  *             served too, but much more slowly if it is a prompt among single tokens
  *   max_len   the longest seq_lens (the grid is made for it; tokens behind are not

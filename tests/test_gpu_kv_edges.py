@@ -5,6 +5,7 @@ import pytest
 
 import deterministic_split_lora_amd as dsl
 from oracle import bf16_to_f64, kv
+from synth import rng_for
 from tests.helpers import bf16_from_gpu, gpu_available, torch
 from tests.kv_helpers import Batch, attend, heads_bf16
 
@@ -140,3 +141,35 @@ def test_drafts_that_are_taken_back(D):
     for name, old in zip(("ks", "vs"), plain):
         now = batch.cache[name][batch.table[:, 0]]
         assert np.all(now[0, :, 1] > old[0, :, 1] + 5) and np.all(now[1, :, 0] > old[1, :, 0] + 5)
+
+
+def any_values(batch, seed):
+    """Codes that are no NaN, and scales within a factor of 2^8."""
+    rng = rng_for(seed, "kv-any")
+    c = batch.cache
+    for name in ("k", "v"):
+        c[name][:] = rng.integers(0, 127, c[name].shape) | rng.integers(0, 2, c[name].shape) << 7
+    for name in ("ks", "vs"):
+        c[name][:] = rng.integers(113, 122, c[name].shape)
+    return batch
+
+
+@pytest.mark.parametrize("D", [64, 128, 256])
+@pytest.mark.parametrize("new,longest", [(1, 2), (2, 2), (1, 8), (3, 8), (5, 8), (1, 100), (20, 100)])
+@pytest.mark.parametrize("chunk", [512, 2048])
+def test_bits_with_a_named_chunk(D, new, longest, chunk):
+    """A sequence alone, with the sizes it has, and beside one twenty times as long and one with more new tokens: the same
+    bits where the chunk is named and the longest run of new tokens times 8 rows lies in the same class."""
+    t = torch()
+    alone = any_values(Batch([(new, 700)], 64, 1, D, seed=2), 2)
+    many = any_values(Batch([(longest, 800), (1, 14000), (new, 700), (1, 1)], 64, 1, D, seed=3), 3)
+    at = longest + 1
+    for p in range(11):
+        for name in ("k", "v", "ks", "vs"):
+            many.cache[name][many.table[2, p]] = alone.cache[name][alone.table[0, p]]
+    q, qg = heads_bf16(many.T, 8, D, 1.0, 4, "q")
+    least = {2: new, 8: max(new, 3), 100: max(new, 9)}[longest]             # of the class
+    a, al = attend(qg[at:at + new], alone.gpu(), least, max_len=700, chunk=chunk)
+    b, bl = attend(qg, many.gpu(), longest, chunk=chunk)
+    assert t.equal(bits(a), bits(b[at:at + new])) and t.equal(bits(al), bits(bl[at:at + new]))
+    assert not bool(t.isnan(b).any())
