@@ -7,7 +7,9 @@ import deterministic_split_lora_amd as dsl
 from oracle import bf16_to_f64, kv
 from synth import rng_for
 from tests.helpers import bf16_from_gpu, gpu_available, torch
-from tests.kv_helpers import Batch, attend, heads_bf16
+from tests.kv_helpers import Batch, attend, heads_bf16, ints
+from tests.test_gpu_kv_append import bf16_round, ready, rope_table
+from tests.test_gpu_kv_attention import check
 
 pytestmark = [pytest.mark.gpu,
               pytest.mark.skipif(not gpu_available(), reason="needs a GPU")]
@@ -173,3 +175,110 @@ def test_bits_with_a_named_chunk(D, new, longest, chunk):
     b, bl = attend(qg, many.gpu(), longest, chunk=chunk)
     assert t.equal(bits(a), bits(b[at:at + new])) and t.equal(bits(al), bits(bl[at:at + new]))
     assert not bool(t.isnan(b).any())
+
+
+SIZES = [(D, P) for D in (64, 128, 256) for P in (16, 64, 128)]
+
+
+def ragged(new, P, D):
+    """Two sequences of these new tokens, one whose pages are all missing, more new tokens than tokens, no token."""
+    return Batch([(new, 200), (new, 100), (2, 30), (3, 2), (1, 0)], P, 2, D, seed=5, rows_behind=2).fill()
+
+
+@pytest.mark.parametrize("D,P", SIZES)
+@pytest.mark.parametrize("new", NEW[:2] + [20])
+def test_pages_that_are_not_there(D, P, new):
+    batch = ragged(new, P, D)
+    batch.table[0, 100 // P] = -1
+    batch.table[0, 199 // P] = batch.n_pages                    # the newest tokens
+    batch.table[1, 0] = 2 ** 31 - 1                             # of the second, at pages of 128, everything
+    batch.table[2, :] = -7
+    q, qg = heads_bf16(batch.T, 16, D, 1.0, 4, "q")
+    g = batch.gpu()
+    check(batch, q, attend(qg, g, new))
+    check(batch, q, attend(qg, g, new, window=40, chunk=256), window=40)
+    check(batch, q, attend(qg, g, new, causal=False), causal=False)
+
+
+@pytest.mark.parametrize("D,P", SIZES)
+@pytest.mark.parametrize("new", NEW[:2] + [20])
+def test_nan_codes(D, P, new):
+    """Values and keys that are NaN, in columns from one end of the head to the other."""
+    batch = ragged(new, P, D)
+
+    def spoil(b, p, h, name, d):
+        page, at = int(batch.table[b, p // P]), p % P
+        if name == "k":
+            batch.cache["k"][page, h, at, d] = 0xFF
+        else:
+            batch.cache["v"][page, h, at // 16, d, at % 16] = 0x7F
+    for d in (0, D // 2 + 5, D - 1):
+        spoil(0, 199, 0, "v", d)                                # the last token: only the last query sees it
+    spoil(0, 200 - (new + 1) // 2, 0, "v", D // 2 - 3)          # one among the new ones
+    spoil(0, 198, 1, "k", D - 1)
+    spoil(1, 20, 1, "v", D - 2)                                 # behind the window below
+    spoil(1, 21, 0, "k", 3)
+    spoil(1, 70, 1, "v", 1)
+    q, qg = heads_bf16(batch.T, 16, D, 1.0, 4, "q")
+    g = batch.gpu()
+    check(batch, q, attend(qg, g, new))
+    check(batch, q, attend(qg, g, new, window=40, chunk=256), window=40)
+    check(batch, q, attend(qg, g, new, causal=False), causal=False)
+
+
+TABLES = [  # offsets, lengths, the sequences whose entries are sound (none: their order is not)
+    ([0, 9, 2, 6], [10, 20, 30], []), ([6, 4, 2, 0], [10, 20, 30], []), ([-5, 2, 4, 6], [10, 20, 30], [1, 2]),
+    ([0, 2, 4, 600], [10, 20, 30], [0, 1]), ([0, 2, 4, 6], [-10, 2 ** 31 - 1, 30], [2]),
+    ([0, 2, 4, 6], [2 ** 31 - 1, 20, -2 ** 31], [1])]
+
+
+@pytest.mark.parametrize("D", [64, 128, 256])
+@pytest.mark.parametrize("cu,lens,sound", TABLES)
+def test_append_with_tables_that_make_no_sense(D, cu, lens, sound):
+    """Sound sequences get what they get among sound ones; nothing else is written, in the pool, between its pages or
+    around the queries."""
+    t = torch()
+    batch = Batch([(2, 10), (2, 20), (2, 30)], 16, 1, D, seed=5).fill()
+    g = batch.gpu(pad=32)
+    g = g._replace(cu_tokens=ints(cu), seq_lens=ints(lens))
+    x, xg = heads_bf16(6, 5, D, 1.0, 1, "x")
+    w = heads_bf16(1, 1, D, 1.0, 2, "w")
+    rope = rope_table(40, D)
+    around = t.full((8, 4, D), 7.0, dtype=t.bfloat16, device="cuda")
+    dsl.lora_kv_append(xg[:, 3:4], xg[:, 4:], g, q=xg[:, :3], q_out=around[1:7, :3], q_norm=w[1].view(-1),
+                       k_norm=w[1].view(-1), rope=t.from_numpy(rope).cuda())
+    t.cuda.synchronize()
+    assert bool((around[[0, 7]] == 7.0).all()) and bool((around[:, 3] == 7.0).all())
+    for a in (g.k, g.v, g.k_scales, g.v_scales):
+        whole = a.as_strided((batch.n_pages, a.stride(0)), (a.stride(0), 1))
+        assert bool((whole[:, a[0].numel():] == 0xEE).all())
+    out = around[1:7, :3].float().cpu().numpy()
+    for b in sound:
+        rows = range(cu[b], cu[b + 1])
+        at = [(b, lens[b] - (cu[b + 1] - i), 0) for i in rows]
+        part = x[list(rows)]
+        k = ready(part[:, 3:4], w[0][0, 0], rope, at, False)
+        kv.append(batch.cache, k, part[:, 4:], batch.table[[b]], [lens[b]], [0, 2], 16)
+        want = bf16_to_f64(bf16_round(ready(part[:, :3], w[0][0, 0], rope, at, False)))
+        assert np.array_equal(out[list(rows)], want)
+    if sound:
+        batch.same(g)
+
+
+@pytest.mark.parametrize("D", [64, 128, 256])
+@pytest.mark.parametrize("new", [1, 5, 40])
+@pytest.mark.parametrize("cu,lens,sound", TABLES)
+def test_attention_with_tables_that_make_no_sense(D, new, cu, lens, sound):
+    t = torch()
+    batch = Batch([(2, 10), (2, 20), (2, 30)], 16, 1, D, seed=5).fill()
+    g = batch.gpu()
+    q, qg = heads_bf16(6, 8, D, 1.0, 4, "q")
+    want, wlse = attend(qg, g, new)
+    bad = g._replace(cu_tokens=ints(cu), seq_lens=ints(lens))
+    for chunk in (0, 256):
+        around = t.full((8, 9, D), 7.0, dtype=t.bfloat16, device="cuda")
+        out, lse = attend(qg, bad, new, out=around[1:7, :8], max_len=700, chunk=chunk)
+        assert bool((around[[0, 7]] == 7.0).all()) and bool((around[:, 8] == 7.0).all())
+        for b in sound:
+            rows = slice(cu[b], cu[b + 1])
+            assert t.equal(bits(out[rows].contiguous()), bits(want[rows])) and t.equal(bits(lse[rows]), bits(wlse[rows]))
