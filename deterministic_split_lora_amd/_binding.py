@@ -727,7 +727,8 @@ def lora_kv_attention(q, cache, out, max_new: int, max_len=None, scale=None, cau
     max_len: the longest run of new tokens and the longest sequence (default: all that the table holds); scale: default
     1 / sqrt(D); chunk: keys that one workgroup joins on its own (0: by these sizes); workspace: tensor of
     lora_kv_attention_workspace_bytes, None if that is 0.  A sequence's bits do not depend on the others of its step where
-    chunk is named and max_new * q_heads / heads stays up to 16, up to 64, or above."""
+    chunk is named and max_new * q_heads / heads stays up to 16, up to 64, or above.  Prompts and single tokens of one step
+    are served better by two calls, on cache._replace(page_table=, seq_lens=, cu_tokens=) of a part of the sequences each."""
     st = (_native_module or _native()).kv_attention(q, cache, out, max_new, max_len, scale, causal, window, chunk, lse,
                                                     workspace, _stream_address(stream, q))
     if st:

@@ -780,7 +780,12 @@ int lora_kv_append(const lora_kv_cache* cache, const uint16_t* q, int64_t ld_q, 
  * another one where max_new or max_len is: a caller whose bits may not depend on the
  * step's other sequences names one.
  *   max_new   the longest run of new tokens: it picks the kernel; a longer one is
- *             served too, but much more slowly if it is a prompt among single tokens
+ *             served too, but much more slowly if it is a prompt among single tokens.
+ *             Single tokens beside a prompt take a prompt's tiles of 128 rows and its
+ *             chunks: two calls on parts of the tables (of page_table, seq_lens and
+ *             cu_tokens, whose first entry need not be 0; the other rows are left as
+ *             they are) take less time than one, 512 tokens against 32768 and 60 single
+ *             ones of up to 16384, 32 heads, 580 us instead of 750
  *   max_len   the longest seq_lens (the grid is made for it; tokens behind are not
  *             seen).  At most 2^30, and taken as max_pages * page_size where that
  *             is less

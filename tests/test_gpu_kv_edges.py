@@ -282,3 +282,45 @@ def test_attention_with_tables_that_make_no_sense(D, new, cu, lens, sound):
         for b in sound:
             rows = slice(cu[b], cu[b + 1])
             assert t.equal(bits(out[rows].contiguous()), bits(want[rows])) and t.equal(bits(lse[rows]), bits(wlse[rows]))
+
+
+@pytest.mark.parametrize("D", [64, 128, 256])
+def test_a_step_in_two_calls(D):
+    """A prompt's tokens and single ones over parts of the batch's tables, each call with its own sizes: every row is
+    served, by the call whose sequences it belongs to."""
+    t = torch()
+    batch = Batch([(30, 90), (1, 40), (1, 130), (1, 7)], 16, 1, D, seed=5, start=1, rows_behind=2).fill()
+    q, qg = heads_bf16(batch.T, 8, D, 1.0, 4, "q")
+    g = batch.gpu()
+    first = g._replace(page_table=g.page_table[:1], seq_lens=g.seq_lens[:1], cu_tokens=g.cu_tokens[:2])
+    rest = g._replace(page_table=g.page_table[1:], seq_lens=g.seq_lens[1:], cu_tokens=g.cu_tokens[1:])
+    out, lse = attend(qg, first, 30, max_len=90)
+    more, mlse = attend(qg, rest, 1, max_len=130)
+    assert bool((out[31:] == 7.0).all()) and bool((more[:31] == 7.0).all())
+    rows = t.arange(batch.T, device="cuda") >= 31
+    check(batch, q, (t.where(rows[:, None, None], more, out), t.where(rows[:, None], mlse, lse)))
+
+
+@pytest.mark.parametrize("D", [64, 128, 256])
+@pytest.mark.parametrize("new", NEW)
+def test_weights_far_below_the_largest(D, new):
+    """A column in which the key of the largest weight has 0: what is left is the second's, with half a step of 2^-40
+    of the largest weight; 2^-8 is the output's half step, and 2^-10 holds the weight's own, 2^-11, and the fp32 ones."""
+    n = max(new, 2)
+    for logit, code in ((-1.0, 0xB8), (-18.0, 0xD9), (-22.0, 0xDB), (-24.0, 0xDC), (-26.0, 0xDD)):
+        assert kv.VALUES[code] == logit
+        batch = Batch([(new, n)], 64, 1, D, seed=5)
+        c, page = batch.cache, batch.table[0, 0]
+        c["k"][page], c["v"][page], c["ks"][page], c["vs"][page] = 0, 0, 127, 110
+        c["k"][page, 0, 1, 0] = code
+        c["k"][page, 0, 2:, 0] = 0xF7                           # -240: nothing of the others
+        c["v"][page, 0, 0, 0, 0] = 0x7E                         # 448, in the first column the first token's
+        c["v"][page, 0, 0, D - 1, 1] = 0x7E                     # in the last one the second's
+        q = torch().zeros(new, 8, D, dtype=torch().bfloat16, device="cuda")
+        q[:, :, 0] = 1.0
+        out = bf16_to_f64(bf16_from_gpu(attend(q, batch.gpu(), new, scale=1.0)[0]))[1 if new > 1 else 0:]
+        w, one = np.exp(logit), 448.0 * 2.0 ** -17
+        first, last = one / (1 + w), one * w / (1 + w)
+        assert np.all(np.abs(out[:, :, 0] - first) <= first * (2.0 ** -8 + 2.0 ** -10))
+        assert np.all(np.abs(out[:, :, D - 1] - last) <= last * (2.0 ** -8 + 2.0 ** -10) + one * 2.0 ** -40), (logit, out[0, 0, D - 1], last)
+        assert not out[:, :, 1:D - 1].any()
