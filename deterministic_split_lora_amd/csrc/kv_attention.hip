@@ -469,7 +469,8 @@ template <int D>
 struct TileLds {
     u32x4 k[2][D / 16][2][kStep];            // bf16: 8 d of a key, for each lane half
     u32x4 v[2][kStep / kKvBlock][2][D];      // fp16: 8 keys of a d, for each lane half
-    int v_exponent[2][kStep / kKvBlock];     // of the blocks' scales, written with K
+    float v_exponent[2][kStep / kKvBlock];   // of the blocks' scales, written with K
+    float v_back[2][kStep / kKvBlock];       // back_of them
     uint32_t nan_step[2];                    // the last step with a value that is NaN
     uint16_t nan[2][kStep / kKvBlock][D];    // then: which keys' value of a d is
 };
@@ -590,7 +591,8 @@ __global__ void __launch_bounds__(kWaves * 64, D == 256 ? 1 : 2) k_attention_til
     };
     auto store_k = [&](int buf) __attribute__((always_inline)) {
         const float s = pow2_of_scale(kscale);
-        lds.v_exponent[buf][wave] = (int)vscale - 127;
+        lds.v_exponent[buf][wave] = (float)((int)vscale - 127);
+        lds.v_back[buf][wave] = back_of((int)vscale);
 #pragma unroll
         for (int j = 0; j < kPieces; ++j) {
             auto& to = lds.k[buf][k_piece + 4 * j];
@@ -668,11 +670,15 @@ __global__ void __launch_bounds__(kWaves * 64, D == 256 ? 1 : 2) k_attention_til
     const int s0 = (int)(begin / kKeys), s1 = (int)((end + kKeys - 1) / kKeys);
     int page_v = -1, page_k = -1;            // of the next step, the one behind it
     uint32_t gone = 0, gone_next = 0, gone_far = 0;    // of this step, the next, the one behind it
-    int e[kBlocks];                          // exponents of the step's V, the same in every lane
+    // of the step's V, the same in every lane: no registers of the vector unit
+    float e[kBlocks], back[kBlocks];
+    auto of_wave = [](float x) { return __builtin_bit_cast(float, __builtin_amdgcn_readfirstlane(__builtin_bit_cast(int, x))); };
     auto exponents = [&](int buf) __attribute__((always_inline)) {
 #pragma unroll
-        for (int u = 0; u < kBlocks; ++u)
-            e[u] = __builtin_amdgcn_readfirstlane(lds.v_exponent[buf][u]);
+        for (int u = 0; u < kBlocks; ++u) {
+            e[u] = of_wave(lds.v_exponent[buf][u]);
+            back[u] = of_wave(lds.v_back[buf][u]);
+        }
     };
     Logits s_even, s_odd;                    // of the even and odd steps from the first on
     if (threadIdx.x < 2)
@@ -711,15 +717,14 @@ __global__ void __launch_bounds__(kWaves * 64, D == 256 ? 1 : 2) k_attention_til
                     s[t][i] = sees ? s[t][i] : -INFINITY;
                 }
         }
-        float top;
+        float top = -INFINITY;
 #pragma unroll
         for (int u = 0; u < kBlocks; ++u) {
-            float of_block = s[u / 2][u % 2 * 8];
+            float of_block = -INFINITY;
 #pragma unroll
-            for (int i = 1; i < 8; ++i)
+            for (int i = 0; i < 8; ++i)
                 of_block = fmaxf(of_block, s[u / 2][u % 2 * 8 + i]);
-            const float scaled = fmaf(of_block, sl, (float)e[u]);
-            top = u ? fmaxf(top, scaled) : scaled;
+            top = fmaxf(top, fmaf(of_block, sl, e[u]));
         }
         const float mn = fmaxf(m, above(half_max(top)));
         if (__any(mn > m)) {
@@ -740,7 +745,7 @@ __global__ void __launch_bounds__(kWaves * 64, D == 256 ? 1 : 2) k_attention_til
         Probs prob;
 #pragma unroll
         for (int u = 0; u < kBlocks; ++u) {
-            const float up = (float)e[u] - shift;
+            const float up = e[u] - shift;
             float sum = 0.0f;                // of the P before their rounding, which lse would show
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
@@ -748,7 +753,7 @@ __global__ void __launch_bounds__(kWaves * 64, D == 256 ? 1 : 2) k_attention_til
                 sum = i ? sum + x : x;
                 prob[u][i] = (_Float16)x;
             }
-            l += __builtin_amdgcn_ldexpf(sum, -kUp - e[u]);
+            l = fmaf(sum, back[u], l);
         }
         store_k(buf);
         output(buf, prob);
