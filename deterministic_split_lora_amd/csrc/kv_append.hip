@@ -22,7 +22,9 @@
 //
 // Measured on MI355X, with the queries: 8190 tokens of 64 + 2 x 8 heads of 128, normed,
 // 78-84 us (364 MB, 4.3-4.6 TB/s: the rate of a large copy); 251 single tokens of 32 + 2 x 8
-// heads 12; one token 5.2 (three rounds of loads that wait for one another, and the launch).
+// heads 12 (105 registers: about 1024 of the 2259 workgroups run at a time, so this is three
+// rounds of what one token takes, most of whose lanes have only V's old codes to move); one
+// token 5.2 (three rounds of loads that wait for one another, and the launch).
 #include "kv_cache.h"
 
 #include <math.h>

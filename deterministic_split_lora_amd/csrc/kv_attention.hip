@@ -8,10 +8,11 @@
 // With e the exponent of a block's value scale, the weight of a key in the second is
 //   P = 2^(S + e - m),  m = max(S + e)      (base 2)
 // so V enters as its codes, exactly, in fp16, and P too: times 2^15, of 11 bits down to
-// 2^-29 of the largest, with steps of 2^-39 of it below.  (As bf16, with the scale in V,
-// P's 8 bits were the larger half of the output's error; prompts took 3-4% less time,
-// few rows the same.)  The sum of the softmax, l = sum 2^(S - m), is taken before that
-// rounding and in fp32, as m and O are.
+// 2^-29 of the largest, with steps of 2^-39 of it below.  (P as bf16, with the scale in
+// V, put the output 0.0019-0.0022 from the formula, where its own rounding alone is
+// 0.0016-0.0017, as it is now; prompts took 3-4% less time, few rows the same.  P as two
+// bf16 parts took 30% more for prompts and 2-7% for few rows.)  The sum of the softmax,
+// l = sum 2^(S - m), is taken before that rounding and in fp32, as m and O are.
 // Key rows are dealt to the products so that lane group g (16 lanes) gets the S
 // of the step's block g, all 16 tokens: these are the P it then supplies, and the
 // tokens of the 16 bytes of V that it loads.  No value changes lanes but for the
@@ -22,9 +23,13 @@
 // bytes: 61 sequences of up to 16384, 64 heads, 280 us (4.6 TB/s; 250, 5.2 TB/s, in chunks
 // of 2048); one of 131071 48 us (5.5 TB/s, of which the last-level cache has a part; 58 when
 // it has none); one of 1025 9.5 (two launches); 32 x 5 drafts, heads of 64, 39.  Many rows,
-// by the matrix cores and the vector unit together: prompts of 8191 and 5119 tokens 805-862
-// us (890-950 TFLOP/s; a large library product of bf16 reaches 1450), 512 tokens against
-// 32768 303-320 (850-900).
+// by the matrix cores and the vector unit together: prompts of 8191 and 5119 tokens 850-880
+// us (870-900 TFLOP/s; a large library product of bf16 reaches 1450; 930-955 us in six
+// passes on their own), 512 tokens against 32768 312-364 by card (750-870).
+// Heads of 256, 4 key heads: a token against 1025 12 us, against 131071 50; 61 of up to
+// 16384, 32 heads, 323 (263 in chunks of 2048); 32 x 5 drafts against up to 6000 121 (88; the
+// codes alone would take 51); 512 tokens against 32768, 16 heads, 500, prompts of 8191 and
+// 5119 tokens 1390 (550 TFLOP/s).
 #include "kv_cache.h"
 
 #include <math.h>
@@ -160,6 +165,8 @@ __device__ __forceinline__ void write_row(const KvAttentionParams& p, int64_t at
 // them is always on its way without registers of its own.
 // A sequence has `tiles` workgroups a head and chunk, enough for max_new tokens; where it has
 // more they go round again.
+// Two tiles of heads of 128 (386 registers) and one of heads of 256 (403) leave one wave a
+// SIMD, half of what the others have; nothing is spilled.
 template <int D, int NT>
 __global__ void __launch_bounds__(kWaves * 64, D * NT <= 128 ? 2 : 1) k_attention(KvAttentionParams p, uint32_t tiles)
 {
@@ -458,8 +465,11 @@ __global__ void __launch_bounds__(kWaves * 64, D * NT <= 128 ? 2 : 1) k_attentio
 // and V's tokens lie in that order, so P goes from one product to the other as it is.
 // While a wave takes the softmax of a step it multiplies the next one (S), which does
 // not depend on it; two workgroups a CU fill each other's gaps.  By counters the matrix
-// cores are busy 42% of the time, the vector unit 50%, LDS 32% (no conflicts); a wave waits
-// for data 24% and for an instruction slot 31% of its time.
+// cores are busy 41% of the time, the vector unit 52%, LDS 33% (no conflicts); a wave waits
+// for data 27% and for an instruction slot 27% of its time.  Heads of 128 fill the 256
+// registers of two waves a SIMD (6 are spilled before the loop and read behind it); heads
+// of 256 fill 512 at one (13 spilled, of which a turn of the loop reads six), with 135 KB
+// of LDS and so one workgroup a CU: that is why they reach 550 TFLOP/s, not 890.
 // ---------------------------------------------------------------------------
 typedef float f32x16 __attribute__((ext_vector_type(16)));
 
@@ -898,10 +908,11 @@ hipError_t launch(const KvAttentionParams& p, hipStream_t st)
 }  // namespace
 
 // About one workgroup a CU for one sequence.  Shorter chunks cost a batch more than they
-// give a sequence alone: 512 keys instead of 256 take one of 1025 from 9.3 to 10.5 us
-// (so it keeps 256), but 61 of up to 16384 from 333 to 280 (2048: 250), 32 drafts of 5
-// tokens from 49 to 39 (2048: 33); one of 131071 takes 56 with 512, 48 with 2048 or 4096,
-// 74 with 8192.
+// give a sequence alone: 512 keys instead of 256 take one of 1025 from 9.5 to 10.8 us
+// (so up to 2048 it keeps 256; one of 2049 to 8192 would gain 0.9 to 1.8 us by it too, from
+// 11.2-11.6), but 61 of up to 16384 from 333 to 280 (2048: 250), 32 drafts of 5 tokens
+// from 49 to 39 (2048: 33); from 12000 on 512 is the faster for one as well (12.0 against
+// 13.8); one of 131071 takes 56 with 512, 48 with 2048 or 4096, 74 with 8192.
 int64_t kv_attention_chunk(int64_t max_new, int32_t q_heads, int32_t kv_heads, int32_t D, int64_t max_len)
 {
     const int G = q_heads / kv_heads, R = tile_rows(max_new, G, D);
